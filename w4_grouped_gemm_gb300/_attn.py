@@ -1,0 +1,201 @@
+"""ctypes binding of the attention-side operators (the C ABI in include/lily_attn.h):
+residual addition with RMSNorm, rotation and paged append, shared-prefix attention.
+
+Argument marshalling only, as in ``_lib``; the checks here are those the library cannot
+make from addresses: element types of index tensors, and that tensors live on the GPU.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import LILY_ERR_INVALID_ARG, LilyError, _check, _ptr, _stream
+
+LILY_DTYPE_F16 = 2
+LILY_DTYPE_E4M3 = 3
+LILY_STATUS_BAD_PAGE = 0x10
+LILY_STATUS_BAD_SLOT = 0x20
+LILY_STATUS_BAD_LEN = 0x40
+
+# Every symbol include/lily_attn.h declares.
+ATTN_EXPORTS = ("lily_attn_add_rmsnorm", "lily_attn_rope_append", "lily_attn_workspace_bytes",
+                "lily_attn_shared_prefix")
+
+_DTYPES = {torch.bfloat16: _lib.LILY_DTYPE_BF16, torch.float32: _lib.LILY_DTYPE_F32,
+           torch.float16: LILY_DTYPE_F16, torch.float8_e4m3fn: LILY_DTYPE_E4M3}
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "w_dtype",
+                                               "out_dtype", "group")]
+                + [("eps", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "res_stride", "res_out_stride",
+                                                 "out_stride")])
+
+
+class Cache(ctypes.Structure):
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+                + [(n, ctypes.c_int32) for n in ("dtype", "n_pages", "page_size", "n_kv_heads",
+                                                 "head_dim")]
+                + [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")])
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "n_q_heads", "rotary_dim", "style")]
+                + [(n, ctypes.c_int64) for n in (
+                    "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
+                    "v_token_stride", "v_head_stride", "qo_token_stride", "qo_head_stride")])
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_seqs", "max_q_len",
+                                               "prefix_len", "max_seq_len", "table_stride")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride",
+                                                 "out_token_stride", "out_head_stride")])
+
+
+_attn = None
+
+
+def _L():
+    global _attn
+    if _attn is None:
+        L = _lib.lib()
+        P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        ref = ctypes.POINTER
+        sig = {
+            "lily_attn_add_rmsnorm": (I, [ref(NormDims), P, P, P, P, P, P, P]),
+            "lily_attn_rope_append": (I, [ref(RopeDims), ref(Cache), P, P, P, P, P, P, P, P, SZ, P]),
+            "lily_attn_workspace_bytes": (SZ, [ref(AttnDims), ref(Cache)]),
+            "lily_attn_shared_prefix": (I, [ref(AttnDims), ref(Cache), P, P, P, P, P, P, P, P, SZ,
+                                            P]),
+        }
+        for name, (res, args) in sig.items():
+            f = getattr(L, name)
+            f.restype = res
+            f.argtypes = args
+        _attn = L
+    return _attn
+
+
+def _refuse(what):
+    raise LilyError(LILY_ERR_INVALID_ARG, what)
+
+
+def _gpu(what, *tensors):
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and not t.is_cuda:
+            _refuse(f"{what}: a tensor is not on the GPU")
+
+
+def _typed(what, name, t, dtype):
+    if t is not None and not isinstance(t, int) and (t.dtype is not dtype or not t.is_contiguous()):
+        _refuse(f"{what}: {name} must be a contiguous {dtype} tensor")
+
+
+def _code(dtype) -> int:
+    if dtype not in _DTYPES:
+        _refuse(f"element type {dtype}")
+    return _DTYPES[dtype]
+
+
+class PagedCache:
+    """Views of a K and a V tensor as a paged cache: [page][token][head][D] (layout "nhd")
+    or [page][head][token][D] ("hnd"), of any page, token and head strides that both share.
+    Keeps the tensors alive; .c is the ctypes struct."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, layout: str = "nhd"):
+        if layout not in ("nhd", "hnd"):
+            _refuse("cache layout")
+        if (k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype
+                or k.stride(3) != 1):
+            _refuse("cache: k and v must be 4-D, alike in shape, strides and type, last stride 1")
+        _gpu("cache", k, v)
+        token, head = (1, 2) if layout == "nhd" else (2, 1)
+        self.k, self.v, self.layout = k, v, layout
+
+        def stride(dim):  # a dimension of size 1 has no step; any valid one serves
+            return k.stride(dim) if k.shape[dim] > 1 else max(8, (k.shape[3] + 7) // 8 * 8)
+
+        self.c = Cache(k.data_ptr(), v.data_ptr(), _code(k.dtype), k.shape[0], k.shape[token],
+                       k.shape[head], k.shape[3], stride(0), stride(head), stride(token))
+
+
+def make_norm_dims(T, d, x_dtype, res_dtype, w_dtype, out_dtype, group=0, eps=1e-6, x_stride=None,
+                   res_stride=None, res_out_stride=None, out_stride=None) -> NormDims:
+    """Dims of lily_attn_add_rmsnorm; types are torch's, strides default to d."""
+    return NormDims(T, d, _code(x_dtype), _code(res_dtype), _code(w_dtype), _code(out_dtype),
+                    group, eps, *(d if s is None else s
+                                  for s in (x_stride, res_stride, res_out_stride, out_stride)))
+
+
+def lily_attn_add_rmsnorm(dims: NormDims, x, residual, weight, residual_out, out, scales=None,
+                          stream=None):
+    """residual_out = x + residual; out = its RMSNorm (see the header)."""
+    _gpu("lily_attn_add_rmsnorm", x, residual, weight, residual_out, out, scales)
+    _check(_L().lily_attn_add_rmsnorm(ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight),
+                                      _ptr(residual_out), _ptr(out), _ptr(scales),
+                                      _stream(stream)), "lily_attn_add_rmsnorm")
+
+
+def _strides(t, what):
+    """(token, head) strides of a [tokens][heads][D] tensor, or zeros for None."""
+    if t is None:
+        return 0, 0
+    if t.dim() != 3 or t.stride(2) != 1:
+        _refuse(f"{what}: [tokens][heads][D] with last stride 1")
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2],
+            t.stride(1) if t.shape[1] > 1 else t.shape[2])
+
+
+def make_rope_dims(q, k, v, q_out, rotary_dim, style=0) -> RopeDims:
+    """Dims of lily_attn_rope_append from its [T][heads][D] tensors (q and q_out, or k and v,
+    may be None)."""
+    some = q if q is not None else k
+    if some is None:
+        _refuse("rope dims: neither q nor k")
+    return RopeDims(some.shape[0], q.shape[1] if q is not None else 0, rotary_dim, style,
+                    *_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"),
+                    *_strides(q_out, "q_out"))
+
+
+def lily_attn_rope_append(dims: RopeDims, cache: PagedCache, q, k, v, positions, slots, inv_freq,
+                          q_out, ws, stream=None):
+    """Rotate q into q_out and k, append k and v at `slots` (see the header)."""
+    what = "lily_attn_rope_append"
+    _gpu(what, q, k, v, positions, slots, inv_freq, q_out, ws)
+    _typed(what, "positions", positions, torch.int32)
+    _typed(what, "slots", slots, torch.int64)
+    _typed(what, "inv_freq", inv_freq, torch.float64)
+    _check(_L().lily_attn_rope_append(ctypes.byref(dims), ctypes.byref(cache.c), _ptr(q), _ptr(k),
+                                      _ptr(v), _ptr(positions), _ptr(slots), _ptr(inv_freq),
+                                      _ptr(q_out), _ptr(ws), ws.numel(), _stream(stream)), what)
+
+
+def make_attn_dims(q, out, n_seqs, max_q_len, prefix_len, max_seq_len, table_stride,
+                   scale) -> AttnDims:
+    """Dims of lily_attn_shared_prefix for [tokens][heads][D] tensors q and out."""
+    return AttnDims(q.shape[0], q.shape[1], n_seqs, max_q_len, prefix_len, max_seq_len,
+                    table_stride, scale, *_strides(q, "q"), *_strides(out, "out"))
+
+
+def lily_attn_workspace_bytes(dims: AttnDims, cache: PagedCache) -> int:
+    return int(_L().lily_attn_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache.c)))
+
+
+def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, q_start, seq_lens,
+                            block_table, out, lse, ws, stream=None):
+    """Attention over the shared prefix and each sequence's own pages (see the header)."""
+    what = "lily_attn_shared_prefix"
+    _gpu(what, q, prefix_pages, q_start, seq_lens, block_table, out, lse, ws)
+    _typed(what, "prefix_pages", prefix_pages, torch.int32)
+    _typed(what, "q_start", q_start, torch.int32)
+    _typed(what, "seq_lens", seq_lens, torch.int32)
+    _typed(what, "block_table", block_table, torch.int32)
+    _check(_L().lily_attn_shared_prefix(ctypes.byref(dims), ctypes.byref(cache.c), _ptr(q),
+                                        _ptr(prefix_pages), _ptr(q_start), _ptr(seq_lens),
+                                        _ptr(block_table), _ptr(out), _ptr(lse), _ptr(ws),
+                                        ws.numel(), _stream(stream)), what)

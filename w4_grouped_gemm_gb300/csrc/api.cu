@@ -8,6 +8,7 @@
 #include <mutex>
 #include <vector>
 
+#include "attn.cuh"
 #include "common.cuh"
 
 namespace lily {
@@ -139,6 +140,12 @@ int check_arch() {
   if (dev >= 0 && dev < 64) arch_seen[dev] = ok ? 1 : -1;
   return ok ? LILY_OK : LILY_ERR_ARCH;
 }
+
+}  // namespace
+
+int device_rc() { return check_arch(); }
+
+namespace {
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? LILY_OK : LILY_ERR_CUDA; }
 
@@ -859,8 +866,8 @@ int lily_moe_profile_read(double* total_ms, int64_t* launches) {
 const char* lily_moe_kernel_name(int kind) {
   static const char* names[] = {"router_gemm", "dec_router", "route", "gateup_gemm",
                                 "down_gemm",   "combine",    "dec_gateup", "dec_down",
-                                "unused",      "rmsnorm",     "unused", "unused",
-                                "router_prep", "router_reduce", "token_rows"};
+                                "add_rmsnorm", "rmsnorm",     "rope_append", "attn_keys",
+                                "router_prep", "router_reduce", "token_rows", "attn_merge"};
   if (kind < 0 || kind >= (int)(sizeof(names) / sizeof(names[0]))) return "unused";
   return names[kind];
 }

@@ -1,0 +1,121 @@
+// attn.cuh -- launch arguments and device helpers of the attention-side
+// kernels (include/lily_attn.h).
+#pragma once
+#include "../../include/lily_attn.h"
+#include "common.cuh"
+
+namespace lily {
+
+// Kinds of the per-kernel event timing beside lily_internal.h's.
+enum AttnKernelKind : int {
+  K_ATTN_NORM = 8,
+  K_ATTN_APPEND = 10,
+  K_ATTN_KEYS = 11,
+  K_ATTN_MERGE = 15,
+};
+
+// ---------------------------------------------------------------- norm
+struct NormArgs {
+  const void* x;
+  const void* res;
+  const void* w;
+  void* res_out;
+  void* out;
+  float* scales;
+  int64_t x_stride, res_stride, res_out_stride, out_stride;
+  int T, d, xt, rt, wt, ot, group;
+  float eps;
+};
+// vec: rows start on 8-element boundaries of every operand and d is a multiple of 8.
+cudaError_t launch_add_rmsnorm(const NormArgs& a, bool vec, cudaStream_t s);
+
+// ---------------------------------------------------------------- rope + append
+struct RopeArgs {
+  const void *q, *k, *v;
+  void *qo, *kc, *vc;
+  const int32_t* pos;
+  const int64_t* slots;
+  const double* inv_freq;
+  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head;
+  int64_t c_page, c_head, c_tok, n_slots;
+  int T, hq, hkv, D, rot, style, page_shift, dtype;
+  uint32_t* status;
+};
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
+
+// LILY_OK on the library's device (compute capability 10.3), else the error code (api.cu).
+int device_rc();
+
+// ---------------------------------------------------------------- attention
+// One set of sequences: the batch's own pages, or the shared prefix as one
+// sequence that every query token belongs to.  A unit is one sequence, one KV
+// head and one block of `rows` query rows (row r of a sequence = token r / G,
+// query head h*G + r % G); units are numbered ((seq * n_kv_heads + h) *
+// row_blocks + block).  The units' tiles of 64 keys form one list that the
+// CTAs share out in equal runs, so a unit may be cut anywhere; the part of
+// unit u that CTA c computed is partial u + c of the set.
+struct AttnSet {
+  const int32_t* q_start;  // NULL: sequence s owns tokens s*max_q_len ...
+  const int32_t* lens;     // NULL: every sequence has max_len keys
+  const int32_t* table;
+  int n_seqs, max_q_len, max_len, table_stride;
+  int rows, row_blocks;    // 16, 32 or 64; ceil(max_q_len * G / rows)
+  int causal;              // query j of q sees keys 0 .. len - q + j
+  int min_share;           // tiles a CTA takes, at least
+  int grid;                // CTAs
+  float* part_o;           // [units + grid][rows][D] normalised partial outputs
+  float* part_lse;         // [units + grid][rows] log2 of their softmax sums
+  int2* runs;              // [units] first and last CTA of a unit (own pages)
+};
+
+struct AttnArgs {
+  const void* q;
+  int64_t q_tok, q_head;
+  int T, hq, hkv, G, D, page_shift, n_pages, f16;
+  float scale_log2;  // softmax scale * log2(e)
+  uint32_t* status;
+};
+
+struct MergeArgs {
+  AttnSet pre, own;
+  int pre_tiles, pre_share;  // key tiles of the prefix and per CTA; 0: no prefix
+  void* out;
+  float* lse;
+  int64_t out_tok, out_head;
+};
+
+constexpr int kAttnTile = 64;      // keys of a tile
+constexpr int kAttnMaxGrid = 512;  // CTAs of a key kernel, at most (sizes the workspace)
+
+// CTAs of the key kernel on the current device for a head of D elements.
+int attn_grid(int D);
+// The partials of one set; first: the call's first launch (attn.cu).
+cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
+                             const CUtensorMap& mv, bool first, cudaStream_t s);
+// Their merge into out and lse.
+cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s);
+
+// ---------------------------------------------------------------- 16-bit elements
+__device__ __forceinline__ float lo16_f32(uint32_t w, bool f16) {
+  return f16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)))
+             : __uint_as_float(w << 16);
+}
+__device__ __forceinline__ float hi16_f32(uint32_t w, bool f16) {
+  return f16 ? __half2float(__ushort_as_half((unsigned short)(w >> 16)))
+             : __uint_as_float(w & 0xFFFF0000u);
+}
+// Two floats rounded to a pair of 16-bit elements (a in the low half).
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) {
+  uint32_t r;
+  if (f16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// One float rounded to a 16-bit element.
+__device__ __forceinline__ uint16_t pack1(float a, bool f16) {
+  return f16 ? __half_as_ushort(__float2half_rn(a)) : __bfloat16_as_ushort(__float2bfloat16_rn(a));
+}
+
+}  // namespace lily

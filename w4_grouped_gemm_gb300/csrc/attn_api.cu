@@ -1,0 +1,344 @@
+// attn_api.cu -- the C ABI of include/lily_attn.h: argument checks, workspace
+// layout and the launches of each call.
+#include <climits>
+#include <cmath>
+
+#include "attn.cuh"
+
+namespace lily {
+namespace {
+
+bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+int rc_of(cudaError_t e) { return e == cudaSuccess ? LILY_OK : LILY_ERR_CUDA; }
+
+constexpr int64_t kMaxStride = (int64_t)1 << 39;
+
+// A stride in elements: at least `least`, below 2^39.
+bool stride_ok(int64_t s, int64_t least) { return s >= least && s < kMaxStride; }
+bool head_stride_ok(int64_t s) { return s >= 0 && s < kMaxStride && s % 8 == 0; }
+
+int check_cache(const lily_attn_cache* c) {
+  if (!c || !c->k || !c->v) return LILY_ERR_INVALID_ARG;
+  if (c->dtype != LILY_DTYPE_BF16 && c->dtype != LILY_DTYPE_F16) return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (c->n_pages < 1 || c->n_kv_heads < 1 || c->head_dim < 1) return LILY_ERR_INVALID_ARG;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 &&
+      c->page_size != 256)
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (c->n_kv_heads > 256 || c->head_dim > 256 || c->head_dim % 8) return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1) return LILY_ERR_INVALID_ARG;
+  if (!head_stride_ok(c->page_stride) || !head_stride_ok(c->head_stride) ||
+      !head_stride_ok(c->token_stride))
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c->k) || !aligned16(c->v)) return LILY_ERR_MISALIGNED;
+  return LILY_OK;
+}
+
+int page_shift(const lily_attn_cache& c) {
+  int s = 4;
+  while ((1 << s) < c.page_size) ++s;
+  return s;
+}
+
+bool is16(int t) { return t == LILY_DTYPE_BF16 || t == LILY_DTYPE_F16; }
+bool is_float(int t) { return is16(t) || t == LILY_DTYPE_F32; }
+int bytes_of(int t) { return t == LILY_DTYPE_F32 ? 4 : t == LILY_DTYPE_E4M3 ? 1 : 2; }
+
+// ---------------------------------------------------------------- attention
+int check_attn_dims(const lily_attn_dims* d, const lily_attn_cache* c) {
+  int rc;
+  if (!d) return LILY_ERR_INVALID_ARG;
+  if ((rc = check_cache(c))) return rc;
+  if (d->n_tokens < 1 || d->n_q_heads < 1 || d->n_seqs < 1 || d->max_q_len < 1 ||
+      d->prefix_len < 0 || d->max_seq_len < 0 || d->table_stride < 0)
+    return LILY_ERR_INVALID_ARG;
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return LILY_ERR_INVALID_ARG;
+  if (d->n_tokens > 65536 || d->n_seqs > 65536 || d->n_q_heads % c->n_kv_heads || d->n_q_heads / c->n_kv_heads > 64)
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (d->prefix_len > INT_MAX - 256 || d->max_seq_len > INT_MAX - 256 ||
+      (int64_t)d->max_seq_len > (int64_t)d->table_stride * c->page_size)
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (!head_stride_ok(d->q_token_stride) || !head_stride_ok(d->q_head_stride) ||
+      !head_stride_ok(d->out_token_stride) || !head_stride_ok(d->out_head_stride))
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  return LILY_OK;
+}
+
+// Rows per unit: 16, 32 or 64, the least that holds `rows` (64 at most).
+int unit_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// The workspace: the status word, then the two sets' partials and the own
+// set's runs.  Sized for the largest grid, so that it does not depend on the
+// device.
+struct AttnLayout {
+  size_t pre_o, pre_lse, own_o, own_lse, runs, total;
+};
+
+void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G) {
+  s = AttnSet{};
+  s.n_seqs = n_seqs;
+  s.max_q_len = max_q_len;
+  s.max_len = max_len;
+  const int64_t rows = (int64_t)max_q_len * G;
+  s.rows = unit_rows(rows);
+  s.row_blocks = (int)((rows + s.rows - 1) / s.rows);
+  s.min_share = 1;
+}
+
+// The sets of a call; false where their units do not fit 31 bits.
+bool make_sets(const lily_attn_dims& d, const lily_attn_cache& c, AttnSet& pre, AttnSet& own,
+               AttnLayout& L) {
+  const int G = d.n_q_heads / c.n_kv_heads;
+  set_shape(pre, 1, d.n_tokens, d.prefix_len, G);
+  // (no sequence has more tokens than the call)
+  const int max_q_len = d.max_q_len < d.n_tokens ? d.max_q_len : d.n_tokens;
+  set_shape(own, d.n_seqs, max_q_len, d.max_seq_len, G);
+  own.causal = max_q_len > 1;
+  size_t off = 256;
+  auto part = [&](const AttnSet& s, size_t& o, size_t& lse) {
+    const int64_t units = (int64_t)s.n_seqs * c.n_kv_heads * s.row_blocks;
+    if (units > INT_MAX / 2) return false;
+    const size_t slots = (size_t)units + kAttnMaxGrid;
+    o = off;
+    off += up256(slots * s.rows * c.head_dim * 4);
+    lse = off;
+    off += up256(slots * s.rows * 4);
+    return true;
+  };
+  L = AttnLayout{};
+  if (d.prefix_len > 0 && !part(pre, L.pre_o, L.pre_lse)) return false;
+  if (d.max_seq_len > 0) {
+    if (!part(own, L.own_o, L.own_lse)) return false;
+    L.runs = off;
+    off += up256((size_t)own.n_seqs * c.n_kv_heads * own.row_blocks * 8);
+  }
+  L.total = off;
+  return true;
+}
+
+// The cache as a 4-D tensor [page][head][token][D]; boxes of 64 dimensions
+// (past D: zeros) by the tokens of a page, 64 at most.
+bool cache_map(CUtensorMap* tm, void* base, const lily_attn_cache& c, uint32_t box_tokens) {
+  const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.page_size, (uint64_t)c.n_kv_heads,
+                            (uint64_t)c.n_pages};
+  const uint64_t strides[3] = {(uint64_t)c.token_stride * 2, (uint64_t)c.head_stride * 2,
+                               (uint64_t)c.page_stride * 2};
+  const uint32_t box[4] = {64, box_tokens, 1, 1};
+  return encode_tiled(tm, c.dtype == LILY_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace lily
+
+using namespace lily;
+
+extern "C" {
+
+int lily_attn_add_rmsnorm(const lily_attn_norm_dims* dims, const void* x, const void* residual,
+                          const void* weight, void* residual_out, void* out, float* scales,
+                          void* stream) {
+  if (!dims || !x || !out) return LILY_ERR_INVALID_ARG;
+  const lily_attn_norm_dims& d = *dims;
+  if (d.T < 1 || d.d < 1) return LILY_ERR_INVALID_ARG;
+  if (d.d > 16384 || !is_float(d.x_dtype) || !is_float(d.res_dtype) || !is_float(d.w_dtype) ||
+      !(is16(d.out_dtype) || d.out_dtype == LILY_DTYPE_E4M3))
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  const bool e4m3 = d.out_dtype == LILY_DTYPE_E4M3;
+  if (e4m3 != (scales != nullptr)) return LILY_ERR_INVALID_ARG;
+  if (e4m3 ? (d.group != 0 && d.group != 64 && d.group != 128) || (d.group && d.d % d.group)
+           : d.group != 0)
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (!(d.eps >= 0.f) || !std::isfinite(d.eps)) return LILY_ERR_INVALID_ARG;
+  if (!stride_ok(d.x_stride, d.d) || !stride_ok(d.out_stride, d.d) ||
+      (residual && !stride_ok(d.res_stride, d.d)) ||
+      (residual_out && !stride_ok(d.res_out_stride, d.d)))
+    return LILY_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, residual, weight, residual_out, out, scales};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LILY_ERR_MISALIGNED;
+  if (const int rc = device_rc()) return rc;
+
+  NormArgs a = {};
+  a.x = x;
+  a.res = residual;
+  a.w = weight;
+  a.res_out = residual_out;
+  a.out = out;
+  a.scales = scales;
+  a.x_stride = d.x_stride;
+  a.res_stride = d.res_stride;
+  a.res_out_stride = d.res_out_stride;
+  a.out_stride = d.out_stride;
+  a.T = d.T;
+  a.d = d.d;
+  a.xt = d.x_dtype;
+  a.rt = d.res_dtype;
+  a.wt = d.w_dtype;
+  a.ot = d.out_dtype;
+  a.group = d.group;
+  a.eps = d.eps;
+  auto whole = [](int64_t stride, int type) { return stride * bytes_of(type) % (8 * (type == LILY_DTYPE_E4M3 ? 1 : 2)) == 0; };
+  const bool vec = d.d % 8 == 0 && whole(d.x_stride, d.x_dtype) && whole(d.out_stride, d.out_dtype) &&
+                   (!residual || whole(d.res_stride, d.res_dtype)) &&
+                   (!residual_out || whole(d.res_out_stride, d.res_dtype));
+  return rc_of(launch_add_rmsnorm(a, vec, (cudaStream_t)stream));
+}
+
+int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache* cache,
+                          const void* q, const void* k, const void* v, const int32_t* positions,
+                          const int64_t* slots, const double* inv_freq, void* q_out,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dims) return LILY_ERR_INVALID_ARG;
+  if (const int rc = check_cache(cache)) return rc;
+  const lily_attn_rope_dims& d = *dims;
+  if (d.T < 1 || d.n_q_heads < 0 || d.rotary_dim < 0) return LILY_ERR_INVALID_ARG;
+  if ((q != nullptr) != (d.n_q_heads > 0) || (q != nullptr) != (q_out != nullptr) ||
+      (k != nullptr) != (v != nullptr) || (!q && !k) || (k && !slots) || !workspace ||
+      (d.rotary_dim && (!positions || !inv_freq)))
+    return LILY_ERR_INVALID_ARG;
+  if (d.rotary_dim % 2 || d.rotary_dim > cache->head_dim || (d.style != 0 && d.style != 1) ||
+      d.n_q_heads > 16384)
+    return LILY_ERR_UNSUPPORTED_SHAPE;
+  const int64_t strides[] = {d.q_token_stride, d.q_head_stride, d.k_token_stride, d.k_head_stride,
+                             d.v_token_stride, d.v_head_stride, d.qo_token_stride, d.qo_head_stride};
+  for (int i = 0; i < 8; ++i) {
+    const bool used = i < 2 || i >= 6 ? q != nullptr : k != nullptr;
+    if (used && !head_stride_ok(strides[i])) return LILY_ERR_UNSUPPORTED_SHAPE;
+  }
+  const void* ptrs[] = {q, k, v, q_out, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LILY_ERR_MISALIGNED;
+  if (!aligned(positions, 4) || !aligned(slots, 8) || !aligned(inv_freq, 8))
+    return LILY_ERR_MISALIGNED;
+  if (workspace_bytes < 256) return LILY_ERR_WORKSPACE_TOO_SMALL;
+  if (const int rc = device_rc()) return rc;
+
+  RopeArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qo = q_out;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.pos = positions;
+  a.slots = slots;
+  a.inv_freq = inv_freq;
+  a.q_tok = d.q_token_stride;
+  a.q_head = d.q_head_stride;
+  a.k_tok = d.k_token_stride;
+  a.k_head = d.k_head_stride;
+  a.v_tok = d.v_token_stride;
+  a.v_head = d.v_head_stride;
+  a.qo_tok = d.qo_token_stride;
+  a.qo_head = d.qo_head_stride;
+  a.c_page = cache->page_stride;
+  a.c_head = cache->head_stride;
+  a.c_tok = cache->token_stride;
+  a.n_slots = (int64_t)cache->n_pages * cache->page_size;
+  a.T = d.T;
+  a.hq = d.n_q_heads;
+  a.hkv = k ? cache->n_kv_heads : 0;
+  a.D = cache->head_dim;
+  a.rot = d.rotary_dim;
+  a.style = d.style;
+  a.page_shift = page_shift(*cache);
+  a.dtype = cache->dtype;
+  a.status = static_cast<uint32_t*>(workspace);
+  return rc_of(launch_rope_append(a, (cudaStream_t)stream));
+}
+
+size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cache* cache) {
+  AttnSet pre, own;
+  AttnLayout L;
+  if (check_attn_dims(dims, cache) || !make_sets(*dims, *cache, pre, own, L)) return 0;
+  return L.total;
+}
+
+int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* cache,
+                            const void* q, const int32_t* prefix_pages, const int32_t* q_start,
+                            const int32_t* seq_lens, const int32_t* block_table, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (const int rc = check_attn_dims(dims, cache)) return rc;
+  const lily_attn_dims& d = *dims;
+  if (!q || !out || !workspace || !seq_lens || (d.prefix_len && !prefix_pages) ||
+      (d.max_seq_len && !block_table))
+    return LILY_ERR_INVALID_ARG;
+  if (!q_start && (int64_t)d.n_seqs * d.max_q_len != d.n_tokens) return LILY_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, out, workspace};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return LILY_ERR_MISALIGNED;
+  const void* words[] = {prefix_pages, q_start, seq_lens, block_table, lse};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return LILY_ERR_MISALIGNED;
+  MergeArgs m = {};
+  AttnLayout L;
+  if (!make_sets(d, *cache, m.pre, m.own, L)) return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < L.total) return LILY_ERR_WORKSPACE_TOO_SMALL;
+  if (const int rc = device_rc()) return rc;
+  const int grid = attn_grid(cache->head_dim);
+  if (grid < 1) return LILY_ERR_CUDA;
+
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  AttnArgs a = {};
+  a.q = q;
+  a.q_tok = d.q_token_stride;
+  a.q_head = d.q_head_stride;
+  a.T = d.n_tokens;
+  a.hq = d.n_q_heads;
+  a.hkv = cache->n_kv_heads;
+  a.G = d.n_q_heads / cache->n_kv_heads;
+  a.D = cache->head_dim;
+  a.page_shift = page_shift(*cache);
+  a.n_pages = cache->n_pages;
+  a.f16 = cache->dtype == LILY_DTYPE_F16;
+  a.scale_log2 = (float)((double)d.scale * 1.4426950408889634);
+  a.status = static_cast<uint32_t*>(workspace);
+  CUtensorMap mk, mv;
+  const uint32_t box = cache->page_size < kAttnTile ? cache->page_size : kAttnTile;
+  if (!cache_map(&mk, cache->k, *cache, box) || !cache_map(&mv, cache->v, *cache, box))
+    return LILY_ERR_CUDA;
+  m.out = out;
+  m.lse = lse;
+  m.out_tok = d.out_token_stride;
+  m.out_head = d.out_head_stride;
+  cudaStream_t s = (cudaStream_t)stream;
+
+  bool first = true;
+  if (d.prefix_len) {
+    AttnSet& p = m.pre;
+    p.table = prefix_pages;
+    p.part_o = reinterpret_cast<float*>(base + L.pre_o);
+    p.part_lse = reinterpret_cast<float*>(base + L.pre_lse);
+    m.pre_tiles = (d.prefix_len + kAttnTile - 1) / kAttnTile;
+    const int64_t total = (int64_t)a.hkv * p.row_blocks * m.pre_tiles;
+    p.grid = (int)(total < grid ? total : grid);
+    const int64_t share = (total + p.grid - 1) / p.grid;
+    if (share > INT_MAX) return LILY_ERR_UNSUPPORTED_SHAPE;
+    m.pre_share = (int)share;
+    if (launch_attn_keys(a, p, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
+    first = false;
+  }
+  if (d.max_seq_len) {
+    AttnSet& o = m.own;
+    o.q_start = q_start;
+    o.lens = seq_lens;
+    o.table = block_table;
+    o.table_stride = d.table_stride;
+    o.part_o = reinterpret_cast<float*>(base + L.own_o);
+    o.part_lse = reinterpret_cast<float*>(base + L.own_lse);
+    o.runs = reinterpret_cast<int2*>(base + L.runs);
+    const int64_t most = (int64_t)a.hkv * o.n_seqs * o.row_blocks *
+                         ((d.max_seq_len + kAttnTile - 1) / kAttnTile);
+    o.grid = (int)(most < grid ? most : grid);
+    if (launch_attn_keys(a, o, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
+  } else {
+    m.own.lens = seq_lens;
+    m.own.n_seqs = 0;
+  }
+  return rc_of(launch_attn_merge(a, m, s));
+}
+
+}  // extern "C"
