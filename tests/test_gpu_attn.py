@@ -170,6 +170,59 @@ def test_many_sequences_and_rows(oracle_lib, seqs, D):
           seed=seqs).go()
 
 
+# more than 64 rows per KV head: the tensor-core kernel of the prefix, whose CTAs take 128 rows (two
+# streams of alternate tiles) or 256 (two row blocks, the last of which may be empty)
+@pytest.mark.parametrize("seqs,hq,hkv", [(65, 1, 1), (13, 5, 1), (128, 1, 1), (129, 2, 2),
+                                         (64, 4, 1), (43, 12, 2), (100, 7, 1)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_wide_rows(oracle_lib, seqs, hq, hkv, D):
+    Batch(hq=hq, hkv=hkv, D=D, own=[1 + i % 3 for i in range(seqs)], prefix=300, page=32,
+          seed=seqs).go()
+
+
+@pytest.mark.parametrize("prefix", [1, 64, 127, 128, 129, 255, 257, 1000, 6001])
+@pytest.mark.parametrize("seqs", [10, 30])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_wide_rows_prefix_lengths(oracle_lib, prefix, seqs, D):
+    Batch(hq=8, hkv=1, D=D, own=[1 + i % 3 for i in range(seqs)], prefix=prefix, dtype=H,
+          seed=prefix).go()
+
+
+@pytest.mark.parametrize("D", [8, 40, 72, 80, 96, 136, 192, 200])
+@pytest.mark.parametrize("dtype", [B, H])
+def test_wide_rows_head_dims(oracle_lib, D, dtype):
+    Batch(dtype=dtype, hq=6, hkv=1, D=D, own=[2] * 25, prefix=700, seed=D).go()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("layout", ["nhd", "hnd"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_wide_rows_pages(oracle_lib, page, layout, D):
+    Batch(page=page, layout=layout, D=D, hq=8, hkv=2, own=[1] * 20, prefix=3 * page + 77,
+          seed=page).go()
+    Batch(page=page, layout=layout, D=D, hq=8, hkv=2, own=[1] * 60, prefix=2000, seed=page).go()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_wide_rows_peaked_and_bad_pages(oracle_lib, D):
+    """A maximum that keeps growing rescales the output; pages outside the cache are skipped, whole
+    tiles of them too."""
+    for seqs in (10, 40):
+        b = Batch(hq=8, hkv=1, D=D, own=[3] * seqs, prefix=900, q_scale=12.0, seed=17)
+        order = b.keys[b.prefix_cells, 0].float().norm(dim=-1).argsort()
+        for c in (b.keys, b.values):
+            c[b.prefix_cells] = c[b.prefix_cells[order]]
+        b.go()
+        b = Batch(hq=8, hkv=1, D=D, own=[3] * seqs, prefix=900, seed=18)
+        bad = [0, 3, 5, *range(16, 32), 56]
+        for i in bad:
+            b.prefix_pages[i] = -1 if i % 2 else 10 ** 7
+        out, lse = b.run(status=lily.LILY_STATUS_BAD_PAGE)
+        keep = torch.tensor([i // 16 not in bad for i in range(900)])
+        b.prefix_cells = b.prefix_cells[keep]
+        b.check(out, lse)
+
+
 def test_batch_that_fills_the_gpu(oracle_lib):
     """More units than CTAs, cut at other places than their ends."""
     Batch(hq=2, hkv=2, D=64, own=[(97 * i) % 700 + 1 for i in range(350)], seed=8).go()

@@ -714,12 +714,12 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
   int np = 0, nw = 0, pr = 0, wrow = 0;
   if (m.pre_tiles) {
     const int r = t * a.G + g;
-    const int64_t u = (int64_t)h * m.pre.row_blocks + r / m.pre.rows;
+    const int64_t u = (int64_t)h * m.pre_blocks + r / m.pre_rows;
     const int64_t c0 = u * m.pre_tiles / m.pre_share;
     const int64_t c1 = ((u + 1) * m.pre_tiles - 1) / m.pre_share;
     p0 = u + c0;
-    np = (int)(c1 - c0) + 1;
-    pr = r % m.pre.rows;
+    np = ((int)(c1 - c0) + 1) * m.pre_streams;
+    pr = r % m.pre_rows;
   }
   {
     int s;
@@ -748,9 +748,13 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
     }
   }
   const int n = np + nw;
+  // row of partial i of the prefix
+  auto pre_row = [&](int i) {
+    return m.pre_streams == 1 ? (p0 + i) * m.pre_slot_rows + pr
+                              : (p0 + (i >> 1)) * m.pre_slot_rows + (i & 1) * 128 + pr;
+  };
   auto lse_of = [&](int i) {
-    return i < np ? m.pre.part_lse[(p0 + i) * m.pre.rows + pr]
-                  : m.own.part_lse[(w0 + i - np) * m.own.rows + wrow];
+    return i < np ? m.pre_lse[pre_row(i)] : m.own.part_lse[(w0 + i - np) * m.own.rows + wrow];
   };
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
@@ -765,7 +769,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
 #pragma unroll 4
   for (int i = warp; i < n; i += warps) {
     const float w = exp2f(lse_of(i) - Z);
-    const float* o = i < np ? m.pre.part_o + ((p0 + i) * m.pre.rows + pr) * a.D
+    if (w == 0.f) continue;  // (a partial that saw nothing has no output)
+    const float* o = i < np ? m.pre_o + pre_row(i) * a.D
                             : m.own.part_o + ((w0 + i - np) * m.own.rows + wrow) * a.D;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -855,7 +860,7 @@ cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_
   // warps for the rows' partials: the prefix's are known here, a sequence's
   // own lengths only on the device
   int n = 1;
-  if (m.pre_tiles) n += m.pre_tiles / m.pre_share + 2;
+  if (m.pre_tiles) n += (m.pre_tiles / m.pre_share + 2) * m.pre_streams;
   int warps = 1;
   while (warps < 8 && warps * 4 < n) warps *= 2;
   const cudaError_t e = launch_pdl(attn_merge_kernel, dim3((unsigned)a.T, (unsigned)a.hq),

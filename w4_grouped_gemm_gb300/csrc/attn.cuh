@@ -62,7 +62,7 @@ struct AttnSet {
   int rows, row_blocks;    // 16, 32 or 64; ceil(max_q_len * G / rows)
   int causal;              // query j of q sees keys 0 .. len - q + j
   int min_share;           // tiles a CTA takes, at least
-  int grid;                // CTAs
+  int grid;                // CTAs; at most one per tile
   float* part_o;           // [units + grid][rows][D] normalised partial outputs
   float* part_lse;         // [units + grid][rows] log2 of their softmax sums
   int2* runs;              // [units] first and last CTA of a unit (own pages)
@@ -76,9 +76,33 @@ struct AttnArgs {
   uint32_t* status;
 };
 
+// The shared prefix on the tensor cores of a batch with more than 64 rows per
+// KV head (attn_tc.cu): units of block_rows rows, numbered h * row_blocks +
+// block, whose 128-key tiles the CTAs share out as above.
+struct TcArgs {
+  const int32_t* pages;
+  int len, tiles, share, total;  // keys; tiles of a unit, of a CTA, of all units
+  int row_blocks, block_rows;    // 256 rows (paired) or 128
+  int paired;
+  int grid;
+  float* part_o;    // [units + grid][attn_tc_rows(D)][D]
+  float* part_lse;  // [units + grid][attn_tc_rows(D)]
+};
+constexpr int kTcKeys = 128;     // keys of a tile
+constexpr int kTcMaxGrid = 160;  // CTAs, at most
+int attn_tc_v_keys(int D);
+int attn_tc_rows(int D);
+cudaError_t launch_attn_prefix_tc(const AttnArgs& a, const TcArgs& p, const CUtensorMap& mk,
+                                  const CUtensorMap& mv, cudaStream_t s);
+
 struct MergeArgs {
-  AttnSet pre, own;
-  int pre_tiles, pre_share;  // key tiles of the prefix and per CTA; 0: no prefix
+  AttnSet own;
+  // the prefix's partials: key tiles of a unit and of a CTA (0: no prefix);
+  // row blocks of a KV head and their rows; rows of a partial, and partials
+  // of one row in it, 128 rows apart (two where streams took alternate tiles)
+  int pre_tiles, pre_share, pre_blocks, pre_rows, pre_slot_rows, pre_streams;
+  const float* pre_o;
+  const float* pre_lse;
   void* out;
   float* lse;
   int64_t out_tok, out_head;

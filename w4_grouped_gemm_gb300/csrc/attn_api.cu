@@ -68,11 +68,19 @@ int check_attn_dims(const lily_attn_dims* d, const lily_attn_cache* c) {
 // Rows per unit: 16, 32 or 64, the least that holds `rows` (64 at most).
 int unit_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// The workspace: the status word, then the two sets' partials and the own
-// set's runs.  Sized for the largest grid, so that it does not depend on the
-// device.
-struct AttnLayout {
-  size_t pre_o, pre_lse, own_o, own_lse, runs, total;
+// Query rows per KV head from which the prefix goes to the tensor-core kernel:
+// above one mma.sync row block.
+constexpr int kTcRows = 64;
+
+// What a call launches, and its workspace: the status word, then the two sets'
+// partials and the own set's runs.  Sized for the largest grid, so that it
+// does not depend on the device.
+struct Plan {
+  bool tc;
+  AttnSet pre, own;  // pre: not on the tensor-core kernel
+  TcArgs ptc;
+  int64_t pre_units, pre_total, own_most;  // units; tiles; tiles at most
+  size_t pre_o, pre_lse, own_o, own_lse, runs, bytes;
 };
 
 void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G) {
@@ -86,34 +94,53 @@ void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G) {
   s.min_share = 1;
 }
 
-// The sets of a call; false where their units do not fit 31 bits.
-bool make_sets(const lily_attn_dims& d, const lily_attn_cache& c, AttnSet& pre, AttnSet& own,
-               AttnLayout& L) {
+// false where the units or tiles do not fit 31 bits.
+bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   const int G = d.n_q_heads / c.n_kv_heads;
-  set_shape(pre, 1, d.n_tokens, d.prefix_len, G);
+  p = Plan{};
+  size_t off = 256;
+  auto partials = [&](int64_t units, int64_t tiles, int64_t max_grid, int rows, size_t& o,
+                      size_t& lse) {
+    const size_t n = (size_t)(units + (tiles < max_grid ? tiles : max_grid));
+    o = off;
+    off += up256(n * rows * c.head_dim * 4);
+    lse = off;
+    off += up256(n * rows * 4);
+  };
+  if (d.prefix_len) {
+    const int64_t rows = (int64_t)d.n_tokens * G;
+    p.tc = rows > kTcRows;
+    if (p.tc) {
+      TcArgs& t = p.ptc;
+      t.paired = rows > 128 && c.head_dim <= 128;
+      t.block_rows = t.paired ? 256 : 128;
+      t.row_blocks = (int)((rows + t.block_rows - 1) / t.block_rows);
+      t.len = d.prefix_len;
+      t.tiles = (d.prefix_len + kTcKeys - 1) / kTcKeys;
+      p.pre_units = (int64_t)c.n_kv_heads * t.row_blocks;
+      p.pre_total = p.pre_units * t.tiles;
+      partials(p.pre_units, p.pre_total, kTcMaxGrid, attn_tc_rows(c.head_dim), p.pre_o, p.pre_lse);
+    } else {
+      set_shape(p.pre, 1, d.n_tokens, d.prefix_len, G);
+      p.pre_units = (int64_t)c.n_kv_heads * p.pre.row_blocks;
+      p.pre_total = p.pre_units * ((d.prefix_len + kAttnTile - 1) / kAttnTile);
+      partials(p.pre_units, p.pre_total, kAttnMaxGrid, p.pre.rows, p.pre_o, p.pre_lse);
+    }
+    if (p.pre_total > INT_MAX / 2) return false;
+  }
   // (no sequence has more tokens than the call)
   const int max_q_len = d.max_q_len < d.n_tokens ? d.max_q_len : d.n_tokens;
-  set_shape(own, d.n_seqs, max_q_len, d.max_seq_len, G);
-  own.causal = max_q_len > 1;
-  size_t off = 256;
-  auto part = [&](const AttnSet& s, size_t& o, size_t& lse) {
-    const int64_t units = (int64_t)s.n_seqs * c.n_kv_heads * s.row_blocks;
-    if (units > INT_MAX / 2) return false;
-    const size_t slots = (size_t)units + kAttnMaxGrid;
-    o = off;
-    off += up256(slots * s.rows * c.head_dim * 4);
-    lse = off;
-    off += up256(slots * s.rows * 4);
-    return true;
-  };
-  L = AttnLayout{};
-  if (d.prefix_len > 0 && !part(pre, L.pre_o, L.pre_lse)) return false;
-  if (d.max_seq_len > 0) {
-    if (!part(own, L.own_o, L.own_lse)) return false;
-    L.runs = off;
-    off += up256((size_t)own.n_seqs * c.n_kv_heads * own.row_blocks * 8);
+  set_shape(p.own, d.n_seqs, max_q_len, d.max_seq_len, G);
+  p.own.causal = max_q_len > 1;
+  const int64_t units = (int64_t)d.n_seqs * c.n_kv_heads * p.own.row_blocks;
+  if (units > INT_MAX / 2) return false;
+  p.own_most = units * ((d.max_seq_len + kAttnTile - 1) / kAttnTile);
+  if (d.max_seq_len) {
+    partials(units, p.own_most, kAttnMaxGrid, p.own.rows, p.own_o, p.own_lse);
+    p.runs = off;
+    off += up256((size_t)units * 8);
   }
-  L.total = off;
+  p.bytes = off;
   return true;
 }
 
@@ -251,10 +278,9 @@ int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache
 }
 
 size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cache* cache) {
-  AttnSet pre, own;
-  AttnLayout L;
-  if (check_attn_dims(dims, cache) || !make_sets(*dims, *cache, pre, own, L)) return 0;
-  return L.total;
+  Plan p;
+  if (check_attn_dims(dims, cache) || !make_plan(*dims, *cache, p)) return 0;
+  return p.bytes;
 }
 
 int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* cache,
@@ -273,10 +299,9 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
   const void* words[] = {prefix_pages, q_start, seq_lens, block_table, lse};
   for (const void* p : words)
     if (!aligned(p, 4)) return LILY_ERR_MISALIGNED;
-  MergeArgs m = {};
-  AttnLayout L;
-  if (!make_sets(d, *cache, m.pre, m.own, L)) return LILY_ERR_UNSUPPORTED_SHAPE;
-  if (workspace_bytes < L.total) return LILY_ERR_WORKSPACE_TOO_SMALL;
+  Plan p;
+  if (!make_plan(d, *cache, p)) return LILY_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < p.bytes) return LILY_ERR_WORKSPACE_TOO_SMALL;
   if (const int rc = device_rc()) return rc;
   const int grid = attn_grid(cache->head_dim);
   if (grid < 1) return LILY_ERR_CUDA;
@@ -297,45 +322,75 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
   a.scale_log2 = (float)((double)d.scale * 1.4426950408889634);
   a.status = static_cast<uint32_t*>(workspace);
   CUtensorMap mk, mv;
-  const uint32_t box = cache->page_size < kAttnTile ? cache->page_size : kAttnTile;
-  if (!cache_map(&mk, cache->k, *cache, box) || !cache_map(&mv, cache->v, *cache, box))
-    return LILY_ERR_CUDA;
+  const uint32_t page = (uint32_t)cache->page_size;
+  auto maps = [&](uint32_t k_rows, uint32_t v_rows) {
+    return cache_map(&mk, cache->k, *cache, page < k_rows ? page : k_rows) &&
+           cache_map(&mv, cache->v, *cache, page < v_rows ? page : v_rows);
+  };
+  cudaStream_t s = (cudaStream_t)stream;
+  MergeArgs m = {};
   m.out = out;
   m.lse = lse;
   m.out_tok = d.out_token_stride;
   m.out_head = d.out_head_stride;
-  cudaStream_t s = (cudaStream_t)stream;
 
   bool first = true;
   if (d.prefix_len) {
-    AttnSet& p = m.pre;
-    p.table = prefix_pages;
-    p.part_o = reinterpret_cast<float*>(base + L.pre_o);
-    p.part_lse = reinterpret_cast<float*>(base + L.pre_lse);
-    m.pre_tiles = (d.prefix_len + kAttnTile - 1) / kAttnTile;
-    const int64_t total = (int64_t)a.hkv * p.row_blocks * m.pre_tiles;
-    p.grid = (int)(total < grid ? total : grid);
-    const int64_t share = (total + p.grid - 1) / p.grid;
-    if (share > INT_MAX) return LILY_ERR_UNSUPPORTED_SHAPE;
-    m.pre_share = (int)share;
-    if (launch_attn_keys(a, p, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
+    float* part_o = reinterpret_cast<float*>(base + p.pre_o);
+    float* part_lse = reinterpret_cast<float*>(base + p.pre_lse);
+    // one tensor-core CTA per SM
+    const int64_t sms = grid / (cache->head_dim <= 128 ? 2 : 1);
+    const int64_t most = !p.tc ? grid : sms < kTcMaxGrid ? sms : kTcMaxGrid;
+    const int used = (int)(p.pre_total < most ? p.pre_total : most);
+    m.pre_share = (int)((p.pre_total + used - 1) / used);
+    m.pre_o = part_o;
+    m.pre_lse = part_lse;
+    cudaError_t e;
+    if (p.tc) {
+      TcArgs& t = p.ptc;
+      t.pages = prefix_pages;
+      t.total = (int)p.pre_total;
+      t.share = m.pre_share;
+      t.grid = used;
+      t.part_o = part_o;
+      t.part_lse = part_lse;
+      m.pre_tiles = t.tiles;
+      m.pre_blocks = t.row_blocks;
+      m.pre_rows = t.block_rows;
+      m.pre_slot_rows = attn_tc_rows(a.D);
+      m.pre_streams = !t.paired && a.D <= 128 ? 2 : 1;
+      if (!maps(kTcKeys, attn_tc_v_keys(a.D))) return LILY_ERR_CUDA;
+      e = launch_attn_prefix_tc(a, t, mk, mv, s);
+    } else {
+      AttnSet& t = p.pre;
+      t.table = prefix_pages;
+      t.grid = used;
+      t.part_o = part_o;
+      t.part_lse = part_lse;
+      m.pre_tiles = (d.prefix_len + kAttnTile - 1) / kAttnTile;
+      m.pre_blocks = t.row_blocks;
+      m.pre_rows = m.pre_slot_rows = t.rows;
+      m.pre_streams = 1;
+      if (!maps(kAttnTile, kAttnTile)) return LILY_ERR_CUDA;
+      e = launch_attn_keys(a, t, mk, mv, first, s);
+    }
+    if (e != cudaSuccess) return LILY_ERR_CUDA;
     first = false;
   }
+  m.own = p.own;
+  m.own.q_start = q_start;
+  m.own.lens = seq_lens;
   if (d.max_seq_len) {
     AttnSet& o = m.own;
-    o.q_start = q_start;
-    o.lens = seq_lens;
     o.table = block_table;
     o.table_stride = d.table_stride;
-    o.part_o = reinterpret_cast<float*>(base + L.own_o);
-    o.part_lse = reinterpret_cast<float*>(base + L.own_lse);
-    o.runs = reinterpret_cast<int2*>(base + L.runs);
-    const int64_t most = (int64_t)a.hkv * o.n_seqs * o.row_blocks *
-                         ((d.max_seq_len + kAttnTile - 1) / kAttnTile);
-    o.grid = (int)(most < grid ? most : grid);
+    o.part_o = reinterpret_cast<float*>(base + p.own_o);
+    o.part_lse = reinterpret_cast<float*>(base + p.own_lse);
+    o.runs = reinterpret_cast<int2*>(base + p.runs);
+    o.grid = (int)(p.own_most < grid ? p.own_most : grid);
+    if (!maps(kAttnTile, kAttnTile)) return LILY_ERR_CUDA;
     if (launch_attn_keys(a, o, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
   } else {
-    m.own.lens = seq_lens;
     m.own.n_seqs = 0;
   }
   return rc_of(launch_attn_merge(a, m, s));
