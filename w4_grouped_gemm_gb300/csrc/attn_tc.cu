@@ -64,24 +64,39 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Shared-memory descriptor of an N-major operand tile with the 128-byte
-// swizzle: rows of 64 elements of N (128 bytes), one row per K; groups of 8
-// rows are 1024 bytes apart (stride offset), blocks of 64 N `block` bytes
-// (leading offset).
-__device__ __forceinline__ uint64_t sdesc_n_major(uint32_t saddr, uint32_t block) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
+// Shared-memory descriptors with the 128-byte swizzle, as a constant high word
+// (stride offset 1024 between groups of 8 rows, version, swizzle) and a low
+// word (address, leading offset) that advances by adding bytes / 16.
+//   K-major (Q, K): rows of 64 elements along K; the leading offset is unused.
+//   N-major (V as it lies): rows of 64 elements of N, one row per key; blocks
+//   of 64 N are `block` bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_n(uint32_t saddr, uint32_t block) {
+  return saddr >> 4 | (block >> 4) << 16;
+}
+// D (+)= A B^T with A in shared memory / in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status) {
-  const bool ok = warp_wait(bar, parity, abort, status);
-  __syncwarp();
-  return ok;
+  return warp_wait_all(bar, parity, abort, status);
 }
 
 // Keeps every use of r after the point (the wait of the load that filled it).
@@ -300,111 +315,149 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       const uint32_t id_qk = fmt;
       const uint32_t id_pv = (F16 ? idesc_f16_f32(128, blocks * 64) : idesc_bf16_f32(128, blocks * 64)) |
                              1u << 16;  // B is N-major
-      int cnt = 0;        // slots taken so far
-      int p_cnt[2] = {0, 0};
-      int seg = 0;
-      bool ok = true;
-      auto take = [&](int j) {  // slot j from here has arrived
-        return warp_wait_all(full((cnt + j) % C::kSlots), ((cnt + j) / C::kSlots) & 1, &abort_s,
-                             a.status);
+      // ring position: slot and the parity of its current filling
+      struct Pos {
+        int slot, par;
+        __device__ void skip(int n) {
+          slot += n;
+          if (slot >= C::kSlots) {
+            slot -= C::kSlots;
+            par ^= 1;
+          }
+        }
       };
-      // S[buf] = Q[g] K^T with K in the slots from `first` on (counted from cnt)
-      auto qk = [&](int g, int buf, int first) {
-        const uint32_t q = base + g * C::kQTile;
-        for (int c = 0; c < blocks; ++c) {
-          if (!(ok = ok && take(first + c))) return;
-          tc_fence_after();
-          const uint32_t k = slots + ((cnt + first + c) % C::kSlots) * kSlot;
-          if (elect_one()) {
+      Pos cur = {0, 0};    // next slot to take
+      int p_par[2] = {0, 0};
+      int q_par = 0;
+      bool ok = true;
+      // One converged poll for everything a group of MMAs needs: n slots from
+      // x and m more from y on, and P of buffer buf (buf < 0: none).
+      auto ready = [&](Pos x, int n, Pos y, int m, int buf) {
+        for (uint32_t tries = 0;; ++tries) {
+          bool r = buf < 0 || mbar_test_wait(p_full(buf), p_par[buf]);
+          Pos i = x;
+          for (int j = 0; j < n; ++j, i.skip(1)) r = r && mbar_test_wait(full(i.slot), i.par);
+          i = y;
+          for (int j = 0; j < m; ++j, i.skip(1)) r = r && mbar_test_wait(full(i.slot), i.par);
+          if (__all_sync(0xffffffffu, r)) break;
+          if ((tries & 255u) == 255u) {
+            // the bounded wait takes over, one barrier after the other
+            bool w = buf < 0 || warp_wait_all(p_full(buf), p_par[buf], &abort_s, a.status);
+            for (int j = 0; j < n && w; ++j, x.skip(1))
+              w = warp_wait_all(full(x.slot), x.par, &abort_s, a.status);
+            for (int j = 0; j < m && w; ++j, y.skip(1))
+              w = warp_wait_all(full(y.slot), y.par, &abort_s, a.status);
+            if (!w) return false;
+            break;
+          }
+        }
+        if (buf >= 0) p_par[buf] ^= 1;
+        tc_fence_after();
+        return true;
+      };
+      // (the next four: by one elected thread)
+      // S[buf] = Q[g] K^T with K in the slots from x on
+      auto qk = [&](int g, int buf, Pos x) {
+        const uint32_t q = desc_k(base + g * C::kQTile), d = tmem + C::kS + 128 * buf;
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c)
+          if (c < blocks) {
+            const uint32_t k = desc_k(slots + x.slot * kSlot);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (c * 64 + i * 16 < a.D)
-                mma_f16(tmem + C::kS + 128 * buf, sdesc_sw128(q + c * 128 * 128 + i * 32),
-                        sdesc_sw128(k + i * 32), id_qk, c | i);
+              mma_ss(d, q + c * (128 * 128 / 16) + 2 * i, k + 2 * i, id_qk, (c | i) != 0);
+            x.skip(1);
           }
-          __syncwarp();
-        }
-        if (elect_one()) mma_commit(s_full(buf));
-        __syncwarp();
+        mma_commit(s_full(buf));
       };
-      // O[g] (+)= P[buf] V with V in the slots from `first` on
-      auto pv = [&](int g, int buf, int first, bool fresh) {
-        ok = ok && warp_wait_all(p_full(buf), p_cnt[buf] & 1, &abort_s, a.status);
-        ++p_cnt[buf];
-        for (int c = 0; c < C::kVSlots; ++c) {
-          if (!(ok = ok && take(first + c))) return;
-          tc_fence_after();
-          const uint32_t v = slots + ((cnt + first + c) % C::kSlots) * kSlot;
-          if (elect_one()) {
+      // O[g] (+)= P[buf] V with V in the slots from x on
+      auto pv = [&](int g, int buf, Pos x, bool fresh) {
+        const uint32_t d = tmem + C::kO + DP * g, pt = tmem + C::kS + 128 * buf;
 #pragma unroll
-            for (int i = 0; i < C::kVKeys / 16; ++i)
-              mma_f16_ts(tmem + C::kO + DP * g, tmem + C::kS + 128 * buf + (c * (C::kVKeys / 16) + i) * 8,
-                         sdesc_n_major(v + i * 2048, C::kVKeys * 128), id_pv,
-                         !fresh || (c | i) != 0);
-          }
-          __syncwarp();
+        for (int c = 0; c < C::kVSlots; ++c) {
+          const uint32_t v = desc_n(slots + x.slot * kSlot, C::kVKeys * 128);
+#pragma unroll
+          for (int i = 0; i < C::kVKeys / 16; ++i)
+            mma_ts(d, pt + (c * (C::kVKeys / 16) + i) * 8, v + i * (2048 / 16), id_pv,
+                   (c | i) != 0 || !fresh);
+          x.skip(1);
         }
-        if (elect_one()) mma_commit(o_full(g));
-        __syncwarp();
+        mma_commit(o_full(g));
       };
-      // slots [first, first + n) are free once the MMAs so far are done
-      auto release = [&](int first, int n) {
-        if (elect_one())
-          for (int j = 0; j < n; ++j) mma_commit(empty((cnt + first + j) % C::kSlots));
-        __syncwarp();
+      // the n slots from x on are free once the MMAs so far are done
+      auto release = [&](Pos x, int n) {
+        for (int j = 0; j < n; ++j, x.skip(1)) mma_commit(empty(x.slot));
       };
       auto q_ready = [&](int g) {
-        ok = ok && warp_wait_all(q_full(g), seg & 1, &abort_s, a.status);
-        tc_fence_after();
+        ok = ok && warp_wait_all(q_full(g), q_par, &abort_s, a.status);
       };
       while (ok && run.next()) {
         const int left = rows_all - run.unit % p.row_blocks * p.block_rows;
         const int n = run.n;
+        q_ready(0);
+        if (C::kGroups == 2) q_ready(1);
+        q_par ^= 1;
         if (paired) {
           const bool two = left > 128;
-          q_ready(0);
-          qk(0, 0, 0);
-          q_ready(1);
-          if (two) qk(1, 1, 0);
-          if (!ok) break;
-          release(0, blocks);
-          cnt += blocks;
-          for (int t = 0; t < n && ok; ++t) {
+          if (!(ok = ok && ready(cur, blocks, cur, 0, -1))) break;
+          if (elect_one()) {
+            qk(0, 0, cur);
+            if (two) qk(1, 1, cur);
+            release(cur, blocks);
+          }
+          __syncwarp();
+          cur.skip(blocks);
+          for (int t = 0; t < n; ++t) {
             const bool more = t + 1 < n;
-            pv(0, 0, 0, t == 0);
-            if (more) qk(0, 0, C::kVSlots);
-            if (two) pv(1, 1, 0, t == 0);
-            if (!ok) break;
-            release(0, C::kVSlots);
-            if (more) {
-              if (two) qk(1, 1, C::kVSlots);
-              if (!ok) break;
-              release(C::kVSlots, blocks);
+            Pos nk = cur;  // the next tile's K
+            nk.skip(C::kVSlots);
+            if (!(ok = ready(cur, C::kVSlots, nk, more ? blocks : 0, 0))) break;
+            if (elect_one()) {
+              pv(0, 0, cur, t == 0);
+              if (more) qk(0, 0, nk);
             }
-            cnt += C::kVSlots + (more ? blocks : 0);
+            __syncwarp();
+            if (two && !(ok = ready(cur, 0, cur, 0, 1))) break;
+            if (elect_one()) {
+              if (two) pv(1, 1, cur, t == 0);
+              release(cur, C::kVSlots);
+              if (more) {
+                if (two) qk(1, 1, nk);
+                release(nk, blocks);
+              }
+            }
+            __syncwarp();
+            cur = nk;
+            if (more) cur.skip(blocks);
           }
         } else {
           // alternate tiles: buffer t & 1, of stream t & 1 where there are two
-          q_ready(0);
-          if (C::kGroups == 2) q_ready(1);
-          for (int t = 0; t < min(2, n) && ok; ++t) {
-            qk(C::kGroups == 2 ? t : 0, t, 0);
-            if (!ok) break;
-            release(0, blocks);
-            cnt += blocks;
+          for (int t = 0; t < min(2, n); ++t) {
+            if (!(ok = ok && ready(cur, blocks, cur, 0, -1))) break;
+            if (elect_one()) {
+              qk(C::kGroups == 2 ? t : 0, t, cur);
+              release(cur, blocks);
+            }
+            __syncwarp();
+            cur.skip(blocks);
           }
           for (int t = 0; t < n && ok; ++t) {
             const int b = t & 1, g = C::kGroups == 2 ? b : 0;
-            pv(g, b, 0, C::kGroups == 2 ? t < 2 : t == 0);
-            if (!ok) break;
-            release(0, C::kVSlots);
-            cnt += C::kVSlots;
-            if (t + 2 < n) {
-              qk(g, b, 0);
-              if (!ok) break;
-              release(0, blocks);
-              cnt += blocks;
+            const bool more = t + 2 < n;
+            Pos nk = cur;
+            nk.skip(C::kVSlots);
+            if (!(ok = ready(cur, C::kVSlots, nk, more ? blocks : 0, b))) break;
+            if (elect_one()) {
+              pv(g, b, cur, C::kGroups == 2 ? t < 2 : t == 0);
+              release(cur, C::kVSlots);
+              if (more) {
+                qk(g, b, nk);
+                release(nk, blocks);
+              }
             }
+            __syncwarp();
+            cur = nk;
+            if (more) cur.skip(blocks);
           }
         }
         // a stream without a tile here still waits for the unit's end, so that
@@ -413,7 +466,6 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           if (elect_one()) mma_commit(s_full(1));
           __syncwarp();
         }
-        ++seg;
       }
       if (!ok) {
         // given up: the MMAs in flight must be done before tensor memory goes
