@@ -15,8 +15,8 @@
 // more than 2^8: until then P is at most 256 instead of 1, which costs no
 // precision, and the rescale (a pass over O in tensor memory) stays rare.
 //
-// Warp 0 brings K and V (TMA boxes of 64 dimensions and one page) into a ring
-// of 16 KB slots; warp 1 issues the MMAs (one elected thread); two groups of
+// Warps 0 and 2 bring K and V (TMA boxes of 64 dimensions and one page) into a
+// ring of slots; warps 1 and 3 issue the MMAs of a stream each; two groups of
 // four warps take the softmax of one stream each, so that one stream's softmax
 // runs under the other's MMAs.  Rows over 128: the streams are the two row
 // blocks and share every K and V tile ("paired"; L2 feeds 32 bytes per clock
@@ -30,20 +30,24 @@ namespace lily {
 namespace {
 
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kSlot = 16384;         // bytes of a ring slot
 constexpr int kMasks = 16;           // tiles whose key masks are kept
-constexpr int kCtrlWarps = 4;        // producer, MMA issuer, two that only balance the registers
+constexpr int kCtrlWarps = 4;        // K, MMAs of stream 0, V, MMAs of stream 1
 
 // DP: head dimension rounded up to 64, 128 or 256.
 template <int DP>
 struct Tc {
   static constexpr int kGroups = DP <= 128 ? 2 : 1;           // softmax groups = streams
   static constexpr int kThreads = 32 * (kCtrlWarps + 4 * kGroups);
-  static constexpr int kVKeys = 128 * 64 / DP;                // keys of a V slot
+  // ring slots of 128 keys x 64 or 128 dimensions of K, or as many bytes of
+  // whole keys of V: a tile is one slot of each, or two where D > 128.  (With
+  // slots of 16 KB the MMA warp spent as long on their barriers as on the MMAs.)
+  static constexpr int kSlot = DP == 64 ? 16384 : 32768;
+  static constexpr int kSlots = DP == 64 ? 11 : 5;
+  static constexpr int kSlotBlocks = DP == 64 ? 1 : 2;        // blocks of 64 dimensions of K
+  static constexpr int kVKeys = kSlot / (DP * 2);             // keys of a V slot
   static constexpr int kVSlots = kKeys / kVKeys;              // V slots of a tile
   static constexpr int kQTile = 128 * DP * 2;                 // 128 rows, blocks of 64 dimensions
   static constexpr int kQBytes = kGroups * kQTile;
-  static constexpr int kSlots = DP == 64 ? 11 : 10;
   static constexpr int kBytes = kQBytes + kSlots * kSlot;
   // tensor memory columns
   static constexpr int kS = 0;        // + 128 * buffer; P in the first 64 columns
@@ -94,9 +98,43 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two floats in a 64-bit register, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Bounded wait of a whole warp, each lane on its own barrier: 2^22 polls of at
+// least 50 cycles; on giving up it sets *abort and the TIMEOUT status.  The loop
+// is a handful of instructions on purpose: with the time limit of the other
+// kernels in line (%globaltimer, a second vote) each wait cost some 250 cycles,
+// even where it passed at once.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status) {
-  return warp_wait_all(bar, parity, abort, status);
+  bool ok = false;
+  for (uint32_t n = 0; n < 1u << 24 && !ok; ++n) ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *abort = 1;
+  set_status(status, LILY_STATUS_TIMEOUT);
+  return false;
 }
 
 // Keeps every use of r after the point (the wait of the load that filled it).
@@ -130,8 +168,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
                           const __grid_constant__ CUtensorMap mv) {
   using C = Tc<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 10];
-  __shared__ uint32_t mask_s[kMasks][4];
+  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 12];
+  __shared__ __align__(16) uint32_t mask_s[kMasks][4];
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
 
@@ -146,19 +184,24 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   auto s_full = [&](int b) { return bar1 + 8 * (2 + b); };  // scores in buffer b
   auto p_full = [&](int b) { return bar1 + 8 * (4 + b); };  // probabilities in buffer b
   auto o_full = [&](int g) { return bar1 + 8 * (6 + g); };  // product added to stream g's output
-  const uint32_t land = bar1 + 8 * 8, drain = bar1 + 8 * 9;
+  auto turn = [&](int g) { return bar1 + 8 * (8 + g); };    // stream g may issue its MMAs
+  const uint32_t land = bar1 + 8 * 10, drain = bar1 + 8 * 11;
 
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 2 * C::kSlots; ++i) mbar_init(bar0 + 8 * i, 1);
+      for (int i = 0; i < C::kSlots; ++i) {
+        mbar_init(full(i), 1);
+        mbar_init(empty(i), C::kGroups);
+      }
       for (int i = 0; i < 2; ++i) {
         mbar_init(q_full(i), 4);
         mbar_init(s_full(i), 1);
         mbar_init(p_full(i), 4);
         mbar_init(o_full(i), 1);
+        mbar_init(turn(i), 1);
       }
       mbar_init(land, 1);
-      mbar_init(drain, 1);
+      mbar_init(drain, C::kGroups);
       fence_mbar_init();
       abort_s = 0;
       prefetch_tensormap(&mk);
@@ -175,6 +218,17 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
 
+  // ring position: slot and the parity of its current filling
+  struct Pos {
+    int slot, par;
+    __device__ void skip(int n) {
+      slot += n;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
+        par ^= 1;
+      }
+    }
+  };
   Run run;
   run.nt = p.tiles;
   run.n = run.before = 0;
@@ -182,289 +236,263 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   run.end = (int)min((long long)p.share * (blockIdx.x + 1), (long long)p.total);
   const int rows_all = a.T * a.G;
   const int blocks = (a.D + 63) / 64;  // of 64 dimensions
+  const int k_slots = (blocks + C::kSlotBlocks - 1) / C::kSlotBlocks;  // K slots of a tile
   const bool paired = p.paired != 0;
 
   if (warp < kCtrlWarps) {
     if (C::kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
+    if (warp == 0 || warp == 2) {
+      // --------------------------------------------------------- producers
+      // One warp for K, one for V: a tile's boxes go out from one lane each
+      // (lane -> slot c of the tile, first key, first dimension), all lanes
+      // polling their own slot.  One warp for both, slot by slot, took 3800
+      // cycles a tile and held the MMAs up.
+      const bool is_v = warp == 2;
       const int ps = a.page_shift;
-      const int k_rows = min(kKeys, 1 << ps), v_rows = min(C::kVKeys, 1 << ps);  // of a box
-      const int k_boxes = kKeys / k_rows;                     // of a K slot
-      const int v_pages = C::kVKeys / v_rows;                 // of a V slot, times `blocks`
+      const int n_slots = is_v ? C::kVSlots : k_slots;
+      const int slot_keys = is_v ? C::kVKeys : kKeys;
+      const int box_rows = min(slot_keys, 1 << ps);
+      const int per_block = slot_keys / box_rows;      // boxes of 64 dimensions
+      const int wide = is_v ? blocks : C::kSlotBlocks;  // blocks of a slot
+      const int per_slot = per_block * wide;            // boxes; at most 32 of a tile
+      const int c = lane / per_slot, in_slot = lane - c * per_slot;
+      const int box = in_slot / wide, blk = in_slot - box * wide;
+      const int dim = 64 * (blk + (is_v ? 0 : c * wide));
+      const int key = (is_v ? c * slot_keys : 0) + box * box_rows;
+      const uint32_t at_slot = (blk * slot_keys + box * box_rows) * 128;
+      const bool active = c < n_slots && dim < a.D;
+      const uint32_t all_boxes = __ballot_sync(0xffffffffu, active);
+      const uint32_t slot_boxes = per_slot == 32 ? ~0u : (1u << per_slot) - 1;  // of slot 0
       const int last = (p.len - 1) >> ps;
-      int cnt = 0, land_phase = 0;
+      const int span = (kKeys + (1 << ps) - 1) >> ps;  // pages of a tile
+      int c_base = -1, c_page = 0;                     // page indices, 32 at a time
+      int land_par = 0;
       bool ok = true;
-      int c_base[2] = {-1, -1}, c_page[2] = {0, 0};  // page indices, 32 at a time, for K and V
-      // the lane's page of a tile (key k of the prefix), -1 where there is none
-      auto page_of = [&](int which, int k0, int k) {
-        const int first = k0 >> ps, span = (kKeys + (1 << ps) - 1) >> ps;
-        if (c_base[which] < 0 || first < c_base[which] || first + span > c_base[which] + 32) {
-          c_base[which] = first;
-          c_page[which] = first + lane <= last ? p.pages[first + lane] : -1;
+      Pos cur = {0, 0};
+      uint32_t used = 0;  // slots that this warp has filled
+      auto load = [&](int h, int t) {
+        const int k0 = t * kKeys, first = k0 >> ps;
+        if (c_base < 0 || first < c_base || first + span > c_base + 32) {
+          c_base = first;
+          c_page = first + lane <= last ? p.pages[first + lane] : -1;
         }
-        const int i = k >> ps;
-        const int pg = __shfl_sync(0xffffffffu, c_page[which], min(max(i - c_base[which], 0), 31));
-        if (i > last) return -1;
-        if (pg < 0 || pg >= a.n_pages) {
-          set_status(a.status, LILY_STATUS_BAD_PAGE);
-          return -1;
+        const int idx = (k0 + min(key, kKeys - 1)) >> ps;
+        const int pg = __shfl_sync(0xffffffffu, c_page, idx - c_base);
+        const bool there = active && idx <= last;
+        const bool good = there && pg >= 0 && pg < a.n_pages;
+        const uint32_t good_m = __ballot_sync(0xffffffffu, good);
+        const bool whole = good_m == all_boxes && k0 + kKeys <= p.len;
+        uint32_t* mask = mask_s[(run.before + t - run.t0) & (kMasks - 1)];
+        uint32_t w = 0xffffffffu;
+        if (!whole) {
+          // valid keys: lane l answers for keys 4l .. 4l+3 (of one page)
+          if (there && !good) set_status(a.status, LILY_STATUS_BAD_PAGE);
+          const int kl = k0 + 4 * lane;
+          const int pl = __shfl_sync(0xffffffffu, c_page, (kl >> ps) - c_base);
+          const int left = pl < 0 || pl >= a.n_pages ? 0 : p.len - kl;
+          w = (left <= 0 ? 0u : left >= 4 ? 15u : (1u << left) - 1) << (4 * (lane & 7));
+          w |= __shfl_xor_sync(0xffffffffu, w, 1);
+          w |= __shfl_xor_sync(0xffffffffu, w, 2);
+          w |= __shfl_xor_sync(0xffffffffu, w, 4);
         }
-        return pg;
-      };
-      auto load_k = [&](int h, int t) {
-        const int k0 = t * kKeys;
-        // valid keys of the tile: lane l answers for keys 4l .. 4l+3 (one page)
-        const int kl = k0 + 4 * lane;
-        const bool there = page_of(0, k0, kl) >= 0;
-        const int left = p.len - kl;
-        const uint32_t four = !there || left <= 0 ? 0u : left >= 4 ? 15u : (1u << left) - 1;
-        uint32_t w = four << (4 * (lane & 7));
-        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        if ((lane & 7) == 0) mask_s[(run.before + t - run.t0) & (kMasks - 1)][lane >> 3] = w;
-        const int c = lane / k_boxes, i = lane - c * k_boxes;
-        const int pg = page_of(0, k0, k0 + i * k_rows);
-        const bool mine = c < blocks && pg >= 0;
-        const uint32_t all = __ballot_sync(0xffffffffu, mine);
+        if (!is_v && (lane & 7) == 0) mask[lane >> 3] = w;
         __syncwarp();
-        for (int j = 0; j < blocks && ok; ++j) {
-          const int slot = (cnt + j) % C::kSlots;
-          ok = wait_warp(empty(slot), (((cnt + j) / C::kSlots) & 1) ^ 1, &abort_s, a.status);
-          if (ok && lane == 0) {
-            const uint32_t boxes = (k_boxes == 32 ? all : all >> (j * k_boxes) & ((1u << k_boxes) - 1));
-            mbar_arrive_expect_tx(full(slot), __popc(boxes) * k_rows * 128);
-          }
-          __syncwarp();
-          if (ok && mine && c == j)
-            tma_load_4d(slots + slot * kSlot + i * k_rows * 128, &mk, c * 64,
-                        k_boxes > 1 ? 0 : k0 & ((1 << ps) - 1), h, pg, full(slot));
-          __syncwarp();
+        Pos mine = cur;
+        mine.skip(min(c, n_slots - 1));
+        const uint32_t slot = slots + mine.slot * C::kSlot;
+        if (!(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.status))) return;
+        const bool cut = is_v && !whole;
+        const uint32_t bar = cut ? land : full(mine.slot);
+        if (cut ? lane == 0 : active && in_slot == 0)
+          mbar_arrive_expect_tx(bar, __popc(cut ? good_m : good_m >> lane & slot_boxes) * box_rows * 128);
+        used |= __reduce_or_sync(0xffffffffu, 1u << mine.slot);  // (a full warp barrier too)
+        if (good) {
+          const int row = (k0 + key) & ((1 << ps) - 1);
+          if (is_v) tma_load_4d(slot + at_slot, &mv, dim, row, h, pg, bar);
+          else tma_load_4d(slot + at_slot, &mk, dim, row, h, pg, bar);
         }
-        if (ok) cnt += blocks;
-      };
-      auto load_v = [&](int h, int t) {
-        const int k0 = t * kKeys;
-        const uint32_t* m = mask_s[(run.before + t - run.t0) & (kMasks - 1)];
-        const bool whole = (m[0] & m[1] & m[2] & m[3]) == 0xffffffffu;
-        const int per = v_pages * blocks;  // boxes of a slot
-        const int c = lane / per, r = lane - c * per;
-        const int i = r / blocks, b = r - i * blocks;
-        const int kv = c * C::kVKeys + i * v_rows;  // first key of the lane's box in the tile
-        const int pg = page_of(1, k0, k0 + min(kv, kKeys - 1));
-        const bool mine = c < C::kVSlots && pg >= 0;
-        const uint32_t all = __ballot_sync(0xffffffffu, mine);
-        for (int j = 0; j < C::kVSlots && ok; ++j) {
-          const int slot = (cnt + j) % C::kSlots;
-          const uint32_t at = slots + slot * kSlot;
-          ok = wait_warp(empty(slot), (((cnt + j) / C::kSlots) & 1) ^ 1, &abort_s, a.status);
-          if (!ok) break;
-          const uint32_t bar = whole ? full(slot) : land;
-          if (lane == 0) {
-            const uint32_t boxes = per == 32 ? all : all >> (j * per) & ((1u << per) - 1);
-            mbar_arrive_expect_tx(bar, __popc(boxes) * v_rows * 128);
+        __syncwarp();
+        if (cut) {
+          // V of keys that are not there may hold anything, and 0 * NaN
+          // would reach every row: it is set to zero before the MMAs see it
+          if (!(ok = wait_warp(land, land_par, &abort_s, a.status))) return;
+          land_par ^= 1;
+          for (int k = 0; k < kKeys; ++k) {
+            if (__shfl_sync(0xffffffffu, w, (k >> 5) * 8) >> (k & 31) & 1u) continue;
+            Pos z = cur;
+            z.skip(k / C::kVKeys);
+            for (int x = lane; x < blocks * 8; x += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               slots + z.slot * C::kSlot +
+                               ((x >> 3) * C::kVKeys + k % C::kVKeys) * 128 + (x & 7) * 16),
+                           "r"(0)
+                           : "memory");
           }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (mine && c == j)
-            tma_load_4d(at + (b * C::kVKeys + i * v_rows) * 128, &mv, b * 64,
-                        (k0 + kv) & ((1 << ps) - 1), h, pg, bar);
-          __syncwarp();
-          if (!whole) {
-            // V of keys that are not there may hold anything, and 0 * NaN
-            // would reach every row: it is set to zero before the MMAs see it
-            ok = wait_warp(land, land_phase, &abort_s, a.status);
-            land_phase ^= 1;
-            if (!ok) break;
-            for (int k = 0; k < C::kVKeys; ++k) {
-              const int key = j * C::kVKeys + k;
-              if (m[key >> 5] >> (key & 31) & 1u) continue;
-              for (int x = lane; x < blocks * 8; x += 32)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 at + ((x >> 3) * C::kVKeys + k) * 128 + (x & 7) * 16),
-                             "r"(0)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full(slot));
-          }
+          if (active && in_slot == 0) mbar_arrive(full(mine.slot));
         }
-        if (ok) cnt += C::kVSlots;
       };
-      // in the order in which the MMAs take them
+      // in the order in which the MMAs take the slots
+      auto step = [&](bool v, int h, int t) {
+        if (!ok) return;
+        if (v == is_v) load(h, t);
+        cur.skip(v ? C::kVSlots : k_slots);
+      };
       while (ok && run.next()) {
         const int h = run.unit / p.row_blocks;
-        load_k(h, run.t0);
-        if (!paired && run.n > 1 && ok) load_k(h, run.t0 + 1);
         const int ahead = paired ? 1 : 2;
+        for (int t = 0; t < min(ahead, run.n); ++t) step(false, h, run.t0 + t);
         for (int t = 0; t < run.n && ok; ++t) {
-          load_v(h, run.t0 + t);
-          if (t + ahead < run.n && ok) load_k(h, run.t0 + t + ahead);
+          step(true, h, run.t0 + t);
+          if (t + ahead < run.n) step(false, h, run.t0 + t + ahead);
         }
       }
       if (!ok && lane == 0) {
         // given up: the copies in flight must land before the memory goes
         int dead = 0;
-        for (int i = max(0, cnt - C::kSlots); i < cnt; ++i)
-          mbar_wait(full(i % C::kSlots), (i / C::kSlots) & 1, &dead, a.status);
+        for (int i = 0; i < C::kSlots; ++i)
+          if (used >> i & 1u) mbar_wait(full(i), i < cur.slot ? cur.par : cur.par ^ 1, &dead, a.status);
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer
-      const uint32_t fmt = F16 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
-      const uint32_t id_qk = fmt;
+    } else if (warp == 1 || C::kGroups == 2) {
+      // ------------------------------------- MMA issuers: one warp per stream
+      // (Issuing blocks until the tensor pipe takes the MMA, and each barrier
+      // costs some 180 cycles; with one warp for both streams the pipe idled a
+      // third of the time.)
+      const int g = warp >> 1;
+      const uint32_t id_qk = F16 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
       const uint32_t id_pv = (F16 ? idesc_f16_f32(128, blocks * 64) : idesc_bf16_f32(128, blocks * 64)) |
                              1u << 16;  // B is N-major
-      // ring position: slot and the parity of its current filling
-      struct Pos {
-        int slot, par;
-        __device__ void skip(int n) {
-          slot += n;
-          if (slot >= C::kSlots) {
-            slot -= C::kSlots;
-            par ^= 1;
-          }
-        }
-      };
-      Pos cur = {0, 0};    // next slot to take
-      int p_par[2] = {0, 0};
-      int q_par = 0;
+      Pos cur = {0, 0};    // slot of the current step
+      uint32_t p_par = 0;  // parity of buffer b's P: bit b
+      int q_par = 0, frees = 1;
       bool ok = true;
-      // One converged poll for everything a group of MMAs needs: n slots from
-      // x and m more from y on, and P of buffer buf (buf < 0: none).
-      auto ready = [&](Pos x, int n, Pos y, int m, int buf) {
-        for (uint32_t tries = 0;; ++tries) {
-          bool r = buf < 0 || mbar_test_wait(p_full(buf), p_par[buf]);
-          Pos i = x;
-          for (int j = 0; j < n; ++j, i.skip(1)) r = r && mbar_test_wait(full(i.slot), i.par);
-          i = y;
-          for (int j = 0; j < m; ++j, i.skip(1)) r = r && mbar_test_wait(full(i.slot), i.par);
-          if (__all_sync(0xffffffffu, r)) break;
-          if ((tries & 255u) == 255u) {
-            // the bounded wait takes over, one barrier after the other
-            bool w = buf < 0 || warp_wait_all(p_full(buf), p_par[buf], &abort_s, a.status);
-            for (int j = 0; j < n && w; ++j, x.skip(1))
-              w = warp_wait_all(full(x.slot), x.par, &abort_s, a.status);
-            for (int j = 0; j < m && w; ++j, y.skip(1))
-              w = warp_wait_all(full(y.slot), y.par, &abort_s, a.status);
-            if (!w) return false;
-            break;
-          }
-        }
-        if (buf >= 0) p_par[buf] ^= 1;
-        tc_fence_after();
-        return true;
+      auto take = [&](Pos x, int n) {  // the n slots from x on have arrived
+        for (int j = 0; j < n && ok; ++j, x.skip(1))
+          ok = wait_warp(full(x.slot), x.par, &abort_s, a.status);
       };
-      // (the next four: by one elected thread)
-      // S[buf] = Q[g] K^T with K in the slots from x on
-      auto qk = [&](int g, int buf, Pos x) {
+      // Two streams issue by turns, P V of a tile and Q K of the next together:
+      // their MMAs and softmaxes so stay out of step, each under the other's.
+      // (Left alone they fall into step and the pipe idles during both
+      // softmaxes.)  The turn is passed on before the last MMAs go out, so that
+      // the other warp wakes up in time.
+      bool turns = false;
+      uint32_t turn_par = g == 0 ? 1 : 0;  // (stream 0 begins)
+      auto my_turn = [&]() {
+        if (turns) ok = ok && wait_warp(turn(g), turn_par, &abort_s, a.status);
+        turn_par ^= turns;
+      };
+      // (the next three: by one elected thread)
+      // the n slots from x on are free once this stream's MMAs so far are
+      // done (and the other stream's too, where it shares them)
+      auto release = [&](Pos x, int n) {
+        for (int j = 0; j < n; ++j, x.skip(1))
+          for (int k = 0; k < frees; ++k) mma_commit(empty(x.slot));
+      };
+      // S[buf] = Q K^T with K in the slots from x on; passes the turn
+      auto qk = [&](int buf, Pos x) {
+        const Pos k_pos = x;
         const uint32_t q = desc_k(base + g * C::kQTile), d = tmem + C::kS + 128 * buf;
+        uint32_t k = desc_k(slots + x.slot * C::kSlot);
 #pragma unroll
         for (int c = 0; c < DP / 64; ++c)
           if (c < blocks) {
-            const uint32_t k = desc_k(slots + x.slot * kSlot);
+            if (c && c % C::kSlotBlocks == 0) {
+              x.skip(1);
+              k = desc_k(slots + x.slot * C::kSlot);
+            }
+            if (turns && c == blocks - 1) mbar_arrive(turn(g ^ 1));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_ss(d, q + c * (128 * 128 / 16) + 2 * i, k + 2 * i, id_qk, (c | i) != 0);
-            x.skip(1);
+              mma_ss(d, q + c * (128 * 128 / 16) + 2 * i,
+                     k + c % C::kSlotBlocks * (128 * 128 / 16) + 2 * i, id_qk, (c | i) != 0);
           }
         mma_commit(s_full(buf));
+        release(k_pos, k_slots);
       };
-      // O[g] (+)= P[buf] V with V in the slots from x on
-      auto pv = [&](int g, int buf, Pos x, bool fresh) {
+      // O (+)= P[buf] V with V in the slots from x on
+      auto pv = [&](int buf, Pos x, bool fresh) {
+        const Pos v_pos = x;
         const uint32_t d = tmem + C::kO + DP * g, pt = tmem + C::kS + 128 * buf;
+        uint32_t v = desc_n(slots + x.slot * C::kSlot, C::kVKeys * 128);
 #pragma unroll
-        for (int c = 0; c < C::kVSlots; ++c) {
-          const uint32_t v = desc_n(slots + x.slot * kSlot, C::kVKeys * 128);
-#pragma unroll
-          for (int i = 0; i < C::kVKeys / 16; ++i)
-            mma_ts(d, pt + (c * (C::kVKeys / 16) + i) * 8, v + i * (2048 / 16), id_pv,
-                   (c | i) != 0 || !fresh);
-          x.skip(1);
+        for (int k = 0; k < 8; ++k) {
+          if (k && k % (C::kVKeys / 16) == 0) {
+            x.skip(1);
+            v = desc_n(slots + x.slot * C::kSlot, C::kVKeys * 128);
+          }
+          mma_ts(d, pt + k * 8, v + k % (C::kVKeys / 16) * (16 * 128 / 16), id_pv, k != 0 || !fresh);
         }
         mma_commit(o_full(g));
-      };
-      // the n slots from x on are free once the MMAs so far are done
-      auto release = [&](Pos x, int n) {
-        for (int j = 0; j < n; ++j, x.skip(1)) mma_commit(empty(x.slot));
-      };
-      auto q_ready = [&](int g) {
-        ok = ok && warp_wait_all(q_full(g), q_par, &abort_s, a.status);
+        release(v_pos, C::kVSlots);
       };
       while (ok && run.next()) {
         const int left = rows_all - run.unit % p.row_blocks * p.block_rows;
         const int n = run.n;
-        q_ready(0);
-        if (C::kGroups == 2) q_ready(1);
+        const bool shared = paired && left > 128;
+        turns = C::kGroups == 2 && (paired ? shared : n > 1);
+        frees = C::kGroups == 2 && !shared ? 2 : 1;
+        if (!(ok = wait_warp(q_full(g), q_par, &abort_s, a.status))) break;
         q_par ^= 1;
-        if (paired) {
-          const bool two = left > 128;
-          if (!(ok = ok && ready(cur, blocks, cur, 0, -1))) break;
-          if (elect_one()) {
-            qk(0, 0, cur);
-            if (two) qk(1, 1, cur);
-            release(cur, blocks);
-          }
-          __syncwarp();
-          cur.skip(blocks);
+        if (g == 1 && !turns) {
+          // nothing for this stream: its softmax warps wait for this, so that
+          // they do not run ahead
+          if (lane == 0) mbar_arrive(s_full(1));
           for (int t = 0; t < n; ++t) {
-            const bool more = t + 1 < n;
-            Pos nk = cur;  // the next tile's K
-            nk.skip(C::kVSlots);
-            if (!(ok = ready(cur, C::kVSlots, nk, more ? blocks : 0, 0))) break;
-            if (elect_one()) {
-              pv(0, 0, cur, t == 0);
-              if (more) qk(0, 0, nk);
-            }
-            __syncwarp();
-            if (two && !(ok = ready(cur, 0, cur, 0, 1))) break;
-            if (elect_one()) {
-              if (two) pv(1, 1, cur, t == 0);
-              release(cur, C::kVSlots);
-              if (more) {
-                if (two) qk(1, 1, nk);
-                release(nk, blocks);
-              }
-            }
-            __syncwarp();
-            cur = nk;
-            if (more) cur.skip(blocks);
+            cur.skip(k_slots);
+            cur.skip(C::kVSlots);
           }
-        } else {
-          // alternate tiles: buffer t & 1, of stream t & 1 where there are two
-          for (int t = 0; t < min(2, n); ++t) {
-            if (!(ok = ok && ready(cur, blocks, cur, 0, -1))) break;
-            if (elect_one()) {
-              qk(C::kGroups == 2 ? t : 0, t, cur);
-              release(cur, blocks);
-            }
-            __syncwarp();
-            cur.skip(blocks);
-          }
-          for (int t = 0; t < n && ok; ++t) {
-            const int b = t & 1, g = C::kGroups == 2 ? b : 0;
-            const bool more = t + 2 < n;
-            Pos nk = cur;
-            nk.skip(C::kVSlots);
-            if (!(ok = ready(cur, C::kVSlots, nk, more ? blocks : 0, b))) break;
-            if (elect_one()) {
-              pv(g, b, cur, C::kGroups == 2 ? t < 2 : t == 0);
-              release(cur, C::kVSlots);
-              if (more) {
-                qk(g, b, nk);
-                release(nk, blocks);
-              }
-            }
-            __syncwarp();
-            cur = nk;
-            if (more) cur.skip(blocks);
-          }
+          continue;
         }
-        // a stream without a tile here still waits for the unit's end, so that
-        // it does not run ahead of the others
-        if (C::kGroups == 2 && ok && (paired ? left <= 128 : n < 2)) {
-          if (elect_one()) mma_commit(s_full(1));
-          __syncwarp();
+        // the ring's order: K of the first `ahead` tiles, then V of a tile and K
+        // of the tile `ahead` after it; alternating streams take every other tile
+        const int ahead = paired ? 1 : 2;
+        const bool every = paired || C::kGroups == 1;
+        for (int t = 0; t < min(ahead, n); ++t) {
+          if (every || t == g) {
+            take(cur, k_slots);
+            my_turn();
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) qk(paired ? g : t, cur);
+            __syncwarp();
+          }
+          cur.skip(k_slots);
+        }
+        for (int t = 0; t < n && ok; ++t) {
+          const bool more = t + ahead < n;
+          Pos nk = cur;
+          nk.skip(C::kVSlots);
+          if (every || (t & 1) == g) {
+            const int buf = paired ? g : t & 1;
+            take(cur, C::kVSlots);
+            if (more && C::kGroups == 2) take(nk, k_slots);
+            ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.status);
+            p_par ^= 1u << buf;
+            my_turn();
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              pv(buf, cur, paired || C::kGroups == 1 ? t == 0 : t < 2);
+              if (more && C::kGroups == 2) qk(buf, nk);
+              if (!more && turns) mbar_arrive(turn(g ^ 1));
+            }
+            __syncwarp();
+            if (more && C::kGroups == 1) {  // (the ring holds less than two tiles)
+              take(nk, k_slots);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) qk(buf, nk);
+              __syncwarp();
+            }
+          }
+          cur = nk;
+          if (more) cur.skip(k_slots);
+        }
+        // with an odd number of turns the other stream would begin next
+        if (turns && g == 1 && !paired && (n & 1)) {
+          my_turn();
+          if (lane == 0) mbar_arrive(turn(0));
         }
       }
       if (!ok) {
@@ -484,7 +512,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
     const int tid = threadIdx.x - 32 * kCtrlWarps - 128 * g;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // tensor memory lane field
     const float c = a.scale_log2;
-    int s_cnt[2] = {0, 0}, o_cnt = 0;
+    uint32_t s_par = 0;  // parity of buffer b's scores: bit b
+    int o_cnt = 0;       // products of this stream
     bool ok = true;
     while (ok && run.next()) {
       const int h = run.unit / p.row_blocks;
@@ -507,101 +536,130 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(g));
 
-      float z = 0.f, m = -INFINITY, l = 0.f;
+      float z = 0.f, l = 0.f;
+      bool have = false;  // z follows a score
       bool any = false;  // a product has been started
       const bool idle = paired && nrows <= 0;
       const int step = !paired && C::kGroups == 2 ? 2 : 1;
       for (int t = step == 2 ? g : 0; t < run.n && !idle; t += step) {
         const int b = paired ? g : t & 1;
-        ok = wait_warp(s_full(b), s_cnt[b] & 1, &abort_s, a.status);
+        ok = wait_warp(s_full(b), s_par >> b & 1u, &abort_s, a.status);
         if (!ok) break;
-        ++s_cnt[b];
+        s_par ^= 1u << b;
+        const uint4 mw = *reinterpret_cast<const uint4*>(mask_s[(run.before + t) & (kMasks - 1)]);
         tc_fence_after();
         uint32_t s[4][32];
         const uint32_t st = tmem + lanes + C::kS + 128 * b;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(st + 32 * i, s[i]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tie(s[i]);
-        const uint32_t* mw = mask_s[(run.before + t) & (kMasks - 1)];
-        const uint32_t mask[4] = {mw[0], mw[1], mw[2], mw[3]};
-        if ((mask[0] & mask[1] & mask[2] & mask[3]) != 0xffffffffu) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(mask[i] >> j & 1u)) s[i][j] = 0xff800000u;  // -inf
-        }
-        float x = m;
-        {
-          float y[4] = {m, m, m, m};
+        const uint32_t mask[4] = {mw.x, mw.y, mw.z, mw.w};
+        const bool masked = (mw.x & mw.y & mw.z & mw.w) != 0xffffffffu;
+        auto cut = [&](int i) {  // keys that are not there
 #pragma unroll
           for (int j = 0; j < 32; ++j)
+            if (!(mask[i] >> j & 1u)) s[i][j] = 0xff800000u;  // -inf
+        };
+        const uint64_t c2 = pair(c, c);
+        uint64_t z2, sum[4];
+        uint32_t w[32];
+        // P of one half (packed arithmetic) and its sums
+        auto exps = [&](int half) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = fmaxf(y[i], __uint_as_float(s[i][j]));
-          x = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-        }
-        const float zx = x == -INFINITY ? 0.f : __fmul_rn(x, c);
-        // a first maximum is taken as it is; a later one only where the
-        // probabilities would pass 2^8 (!(<=): infinities and NaN too)
-        const bool grow = m != -INFINITY && !(zx - z <= 8.f);
-        float f = 1.f;
-        if (m == -INFINITY) {
-          z = zx;
-          m = x;
-        } else if (grow) {
-          f = ex2(z - zx);
-          z = zx;
-          m = x;
-        }
-        if (__any_sync(0xffffffffu, grow) && any) {
-          // O *= f, after the product that is under way
-          ok = wait_warp(o_full(g), (o_cnt - 1) & 1, &abort_s, a.status);
-          if (!ok) break;
-          tc_fence_after();
-          l *= f;
-          for (int i = 0; i < blocks * 2; ++i) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lanes + C::kO + DP * g + 32 * i, o);
-            tmem_ld_wait();
-            tie(o);
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(tmem + lanes + C::kO + DP * g + 32 * i, o);
+            for (int j = 0; j < 32; j += 2) {
+              const uint32_t* v = s[2 * half + i];
+              float p0, p1;
+              unpair(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), c2, z2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[(j / 2) & 3] = add2(sum[(j / 2) & 3], pair(p0, p1));
+              w[16 * i + j / 2] = pack16(p0, p1, F16);
+            }
+        };
+        tmem_ld32(st, s[0]);
+        tmem_ld32(st + 32, s[1]);
+        tmem_ld_wait();
+        tie(s[0]);
+        tie(s[1]);
+        tmem_ld32(st + 64, s[2]);
+        tmem_ld32(st + 96, s[3]);
+        if (masked) {
+          cut(0);
+          cut(1);
+        }
+        // The first half is taken with the z of the tiles before, under which
+        // the tile's maximum is found; only where that shows z to be more than
+        // 2^8 behind (always at first) z moves, O is rescaled and the half taken
+        // again.
+        for (int pass = 0;; ++pass) {
+          z2 = pair(-z, -z);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = 0;
+          exps(0);
+          if (pass) break;
+          tmem_ld_wait();
+          tie(s[2]);
+          tie(s[3]);
+          if (masked) {
+            cut(2);
+            cut(3);
           }
-          tmem_st_wait();
-        }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float y[8];
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          uint32_t w[32];
+          for (int k = 0; k < 8; ++k) y[k] = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float a0 = ex2(fmaf(__uint_as_float(s[i][j]), c, -z));
-            const float a1 = ex2(fmaf(__uint_as_float(s[i][j + 1]), c, -z));
-            const float b0 = ex2(fmaf(__uint_as_float(s[i + 1][j]), c, -z));
-            const float b1 = ex2(fmaf(__uint_as_float(s[i + 1][j + 1]), c, -z));
-            sum[0] += a0;
-            sum[1] += a1;
-            sum[2] += b0;
-            sum[3] += b1;
-            w[j / 2] = pack16(a0, a1, F16);
-            w[16 + j / 2] = pack16(b0, b1, F16);
+          for (int j = 0; j < 32; j += 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[i] = max3(y[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
+              y[4 + i] = max3(y[4 + i], __uint_as_float(s[i][j + 2]), __uint_as_float(s[i][j + 3]));
+            }
+          const float zx =
+              __fmul_rn(max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), fmaxf(y[6], y[7])), c);
+          // (!(<=): infinities and NaN too)
+          const bool grow = have ? !(zx - z <= 8.f) : zx != -INFINITY;
+          if (!__any_sync(0xffffffffu, grow)) break;
+          const float f = grow && have ? ex2(z - zx) : 1.f;
+          if (grow) {
+            z = zx;
+            have = true;
           }
-          tmem_st32(st + 16 * i, w);
+          if (any) {
+            // O *= f, after the product that is under way
+            ok = wait_warp(o_full(g), (o_cnt - 1) & 1, &abort_s, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            l *= f;
+            for (int i = 0; i < blocks * 2; ++i) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lanes + C::kO + DP * g + 32 * i, o);
+              tmem_ld_wait();
+              tie(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(tmem + lanes + C::kO + DP * g + 32 * i, o);
+            }
+            tmem_st_wait();
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (!ok) break;
+        tmem_st32(st, w);
+        exps(1);
+        tmem_st32(st + 32, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(b));
+        {
+          float u, v;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, v);
+          l += u + v;
+        }
         any = true;
         ++o_cnt;
       }
       if (ok && C::kGroups == 2 && g == 1 && (idle || (!paired && run.n < 2))) {
-        ok = wait_warp(s_full(1), s_cnt[1] & 1, &abort_s, a.status);
-        ++s_cnt[1];
+        ok = wait_warp(s_full(1), s_par >> 1 & 1u, &abort_s, a.status);
+        s_par ^= 2u;
       }
       if (!ok) break;
 
@@ -634,6 +692,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       if (live) p.part_lse[slot_row] = l == 0.f ? -INFINITY : z + log2f(l);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
@@ -651,7 +710,7 @@ cudaError_t launch_tc_as(const AttnArgs& a, const TcArgs& p, const CUtensorMap& 
 }  // namespace
 
 // Keys of a V slot: the largest box of V.
-int attn_tc_v_keys(int D) { return D <= 64 ? 128 : D <= 128 ? 64 : 32; }
+int attn_tc_v_keys(int D) { return D <= 128 ? 128 : 64; }
 // Rows of a partial: two streams of 128, or one.
 int attn_tc_rows(int D) { return D <= 128 ? 256 : 128; }
 
