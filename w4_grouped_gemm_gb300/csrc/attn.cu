@@ -65,14 +65,6 @@ struct alignas(16) Desc {
   int tiles, pad[3];
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
-                                            int c2, int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(tm), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -100,11 +92,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // Byte offset of 16-byte piece c (0..7) of row r in a tile of 128-byte rows
 // with the 128-byte swizzle (tile base 1024-byte aligned).
@@ -139,13 +126,6 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnSet& s, int T, int i) {
   }
   return r;
 }
-// warp_wait, with the whole warp ordered after it.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
-  const bool ok = warp_wait(bar, parity, abort, status);
-  __syncwarp();
-  return ok;
-}
 // Units and tiles of a sequence: row blocks per KV head, and tiles per unit.
 __device__ __forceinline__ int blocks_of(const AttnSet& s, int G, int qn) {
   return (qn * G + s.rows - 1) / s.rows;
@@ -164,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
   __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * C::kQBufs];
   __shared__ Desc desc[C::kQBufs];
   __shared__ unsigned long long mask_s[C::kStages];  // valid keys of a stage
-  __shared__ long long total_s[kWarps + 1];
+  __shared__ int total_s[kWarps + 1];
   __shared__ float red_z[kWarps][16], red_l[kWarps][16];
   __shared__ int abort_s;
   __shared__ int dead_s[2];  // compute warps agree at each unit whether to go on
@@ -207,80 +187,107 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
   if (first) pdl_wait();
   pdl_trigger();
 
-  // the set's tiles, and this CTA's run of them
-  long long sum = 0;
+  // the set's tiles (31 bits: checked on the host), and this CTA's run of them
+  auto cost_of = [&](const SeqInfo& q) { return a.hkv * blocks_of(set, a.G, q.qn) * tiles_of(q.len); };
+  int sum = 0;
   for (int i = threadIdx.x; i < set.n_seqs; i += kThreads) {
     const SeqInfo q = seq_info(set, a.T, i);
     if (q.bad && blockIdx.x == 0) set_status(a.status, LILY_STATUS_BAD_LEN);
-    sum += (long long)a.hkv * blocks_of(set, a.G, q.qn) * tiles_of(q.len);
+    sum += cost_of(q);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) total_s[warp] = sum;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w <= kWarps; ++w) total += total_s[w];
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)set.min_share);
-  const long long begin = share * blockIdx.x;
-  const long long end = min(begin + share, total);
+  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, set.min_share);
+  const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)total);
+  const int end = min(begin + share, total);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
+    // Short sequences make this warp the bottleneck, so it keeps global memory
+    // latency off its path: 32 sequences' lengths lie in the lanes, the next
+    // sequence's first pages are requested a sequence ahead.
     int stage = 0, phase = 0, seg = 0;
     bool ok = true;
     uint32_t used = 0;  // stages filled at least once
-    long long at = begin;
-    int s = 0;
-    long long s_base = 0;  // first tile of sequence s
-    // the sequence of tile `begin`
-    if (begin < end) {
-      for (int b = 0;; b += 32) {
-        long long c = 0;
-        if (b + lane < set.n_seqs) {
-          const SeqInfo q = seq_info(set, a.T, b + lane);
-          c = (long long)a.hkv * blocks_of(set, a.G, q.qn) * tiles_of(q.len);
-        }
-        long long inc = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, s_base + inc > begin);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          s = b + l;
-          s_base += __shfl_sync(0xffffffffu, inc - c, l);
-          break;
-        }
-        s_base += __shfl_sync(0xffffffffu, inc, 31);
-        if (b + 32 >= set.n_seqs) {  // not reached: the lengths add up to `total`
-          at = end;
-          break;
-        }
-      }
-    }
     const int ps = a.page_shift;
     const int box_rows = min(kTile, 1 << ps);
     const int pages_per_tile = kTile / box_rows;
     const uint32_t box_bytes = box_rows * 128;
-    while (ok && at < end && s < set.n_seqs) {
-      const SeqInfo q = seq_info(set, a.T, s);
-      const int nt = tiles_of(q.len), nb = blocks_of(set, a.G, q.qn);
-      const long long cost = (long long)a.hkv * nb * nt;
-      if (at >= s_base + cost) {
-        s_base += cost;
-        ++s;
-        continue;
+    // lane l: page l / (2 halves) of a tile, K or V, half of the head
+    const int i = lane / (2 * halves), rest = lane - i * 2 * halves;
+    const bool is_v = rest >= halves;
+    const int hf = rest - (is_v ? halves : 0);
+    const uint32_t at_stage = (is_v ? C::kTileBytes : 0) + hf * C::kHalfBytes + i * box_bytes;
+
+    int at = begin;
+    int s0 = -1, s = 0;       // sequences s0 .. s0 + 31 lie in the lanes; current one
+    int s_base = 0;           // first tile of sequence s
+    SeqInfo mine = {};        // of sequence s0 + lane
+    int my_cost = 0, my_base = 0;
+    auto load32 = [&](int first_seq, int base_tile) {
+      s0 = first_seq;
+      mine = SeqInfo{};
+      if (s0 + lane < set.n_seqs) mine = seq_info(set, a.T, s0 + lane);
+      my_cost = s0 + lane < set.n_seqs ? cost_of(mine) : 0;
+      int inc = my_cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
       }
-      const int in_seq = (int)((at - s_base) / nt);  // unit of the sequence
-      const int t0 = (int)((at - s_base) - (long long)in_seq * nt);
-      const int nseg = (int)min((long long)(nt - t0), end - at);
+      my_base = base_tile + inc - my_cost;
+    };
+    // the sequence that holds tile t, from the current group on; false past the last
+    auto find = [&](int t) {
+      for (;;) {
+        const uint32_t in = __ballot_sync(0xffffffffu, my_cost > 0 && my_base + my_cost > t);
+        if (in) {
+          s = s0 + __ffs(in) - 1;
+          s_base = __shfl_sync(0xffffffffu, my_base, s - s0);
+          return true;
+        }
+        if (s0 + 32 >= set.n_seqs) return false;
+        load32(s0 + 32, __shfl_sync(0xffffffffu, my_base + my_cost, 31));
+      }
+    };
+    // page indices of the current sequence from page pbase on, and of the next one
+    auto first_pages = [&](int seq, int page) {
+      const int n = seq < s0 + 32 && seq < set.n_seqs ? __shfl_sync(0xffffffffu, mine.len, seq - s0) : 0;
+      const int p = page + lane;
+      return n > 0 && p <= (n - 1) >> ps ? set.table[(int64_t)seq * set.table_stride + p] : -1;
+    };
+    int pseq = -1, pbase = 0, pcache = 0, next_cache = 0;
+    if (at < end) {
+      load32(0, 0);
+      ok = find(at);
+    }
+    while (ok && at < end) {
+      SeqInfo q;
+      q.q0 = __shfl_sync(0xffffffffu, mine.q0, s - s0);
+      q.qn = __shfl_sync(0xffffffffu, mine.qn, s - s0);
+      q.len = __shfl_sync(0xffffffffu, mine.len, s - s0);
+      const int nt = tiles_of(q.len), nb = blocks_of(set, a.G, q.qn);
+      const int in_seq = (at - s_base) / nt;  // unit of the sequence
+      const int t0 = (at - s_base) - in_seq * nt;
+      const int nseg = min(nt - t0, end - at);
       const int h = in_seq / nb, blk = in_seq - h * nb;
       const int unit = (s * a.hkv + h) * set.row_blocks + blk;
       const int row0 = blk * C::kRows;
       const int nrows = min(C::kRows, q.qn * a.G - row0);
+      const int last = (q.len - 1) >> ps;
+      if (s != pseq) {
+        // a sequence's first pages came with the one before it, if it was that
+        // one's neighbour and starts here
+        const bool have = pseq >= 0 && s == pseq + 1 && t0 == 0 && s > s0;
+        pbase = (t0 * kTile) >> ps;
+        pcache = have ? next_cache : first_pages(s, pbase);
+        next_cache = first_pages(s + 1, 0);
+        pseq = s;
+      }
 
       const int qb = seg % C::kQBufs;
       ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.status);
@@ -297,10 +304,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
         d.key0 = t0 * kTile;
         d.tiles = nseg;
         desc[qb] = d;
-        if (t0 == 0 && set.runs) {
-          const long long u0 = s_base + (long long)in_seq * nt;
-          set.runs[unit] = make_int2((int)blockIdx.x, (int)((u0 + nt - 1) / share));
-        }
         mbar_arrive_expect_tx(qfull(qb), nrows * a.D * 2);
       }
       __syncwarp();
@@ -310,27 +313,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(q.q0 + j) * a.q_tok +
                               (int64_t)(h * a.G + g) * a.q_head;
         bulk_load(base + C::kQOff + qb * C::kQBytes + r * C::kQPitch, src, a.D * 2, qfull(qb));
+        if (t0 == 0 && set.rows_at) {
+          // where the merge finds this row's partials: the unit's first, and how many
+          const int u0 = s_base + in_seq * nt;
+          set.rows_at[(int64_t)(q.q0 + j) * a.hq + h * a.G + g] =
+              make_int4(unit + (int)blockIdx.x, r, (u0 + nt - 1) / share - (int)blockIdx.x + 1, s);
+        }
       }
       ++seg;
 
-      // page indices, 32 at a time
-      const int32_t* table = set.table + (int64_t)s * set.table_stride;
-      const int last = (q.len - 1) >> ps;
-      int pbase = -1, pcache = 0;
       for (int t = 0; t < nseg; ++t) {
         const int k0 = (t0 + t) * kTile;
         const int p0 = k0 >> ps;
-        if (pbase < 0 || p0 + pages_per_tile > pbase + 32) {
+        if (p0 < pbase || p0 + pages_per_tile > pbase + 32) {
           pbase = p0;
-          pcache = p0 + lane <= last ? table[p0 + lane] : -1;
+          pcache = first_pages(s, pbase);
         }
-        // lane l: page l / (2 halves) of the tile, K or V, half of the head
-        const int i = lane / (2 * halves), rest = lane - i * 2 * halves;
         const int pg = __shfl_sync(0xffffffffu, pcache, min(p0 + min(i, pages_per_tile - 1) - pbase, 31));
-        const bool mine = i < pages_per_tile && p0 + i <= last;
-        const bool good = mine && pg >= 0 && pg < a.n_pages;
+        const bool there = i < pages_per_tile && p0 + i <= last;
+        const bool good = there && pg >= 0 && pg < a.n_pages;
         const uint32_t good_m = __ballot_sync(0xffffffffu, good);
-        if (mine && !good) set_status(a.status, LILY_STATUS_BAD_PAGE);
+        if (there && !good) set_status(a.status, LILY_STATUS_BAD_PAGE);
         ok = wait_warp(empty(stage), phase ^ 1, &abort_s, a.status);
         if (!ok) break;
         if (lane == 0) {
@@ -344,12 +347,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
         }
         __syncwarp();
         if (good) {
-          const bool v = rest >= halves;
-          const int hf = rest - (v ? halves : 0);
-          const uint32_t dst = base + stage * C::kStageBytes + (v ? C::kTileBytes : 0) +
-                               hf * C::kHalfBytes + i * box_bytes;
+          const uint32_t dst = base + stage * C::kStageBytes + at_stage;
           const int row = pages_per_tile > 1 ? 0 : k0 & ((1 << ps) - 1);
-          if (v) tma_load_4d(dst, &mv, hf * 64, row, h, pg, full(stage));
+          if (is_v) tma_load_4d(dst, &mv, hf * 64, row, h, pg, full(stage));
           else tma_load_4d(dst, &mk, hf * 64, row, h, pg, full(stage));
         }
         __syncwarp();
@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
         }
       }
       at += nseg;
+      if (ok && at < end && at >= s_base + a.hkv * nb * nt) ok = find(at);
     }
     // no more units
     if (ok) {
@@ -375,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
       int dead = 0;
       if (seg > 0)
         mbar_wait(qfull((seg - 1) % C::kQBufs), ((seg - 1) / C::kQBufs) & 1, &dead, a.status);
-      for (int i = 0; i < C::kStages; ++i)
-        if (used >> i & 1u) mbar_wait(full(i), i < stage ? phase : phase ^ 1, &dead, a.status);
+      for (int j = 0; j < C::kStages; ++j)
+        if (used >> j & 1u) mbar_wait(full(j), j < stage ? phase : phase ^ 1, &dead, a.status);
     }
   } else {
     // ------------------------------------------------------------- compute
@@ -404,8 +405,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
       if (C::kQRegs) {
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks) ldsm4(qaddr + ks * 32, qf[ks]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(qb));
       }
       const bool busy = wr * 16 < d.nrows;
       // keys that each of the thread's two rows sees
@@ -595,7 +594,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(stage));
+        if (lane == 0) {
+          mbar_arrive(empty(stage));
+          // The first tile's products have used the fragments of Q: only now is
+          // the buffer free.  (Released right after the loads were issued, the
+          // next rows could land before these were read.)
+          if (C::kQRegs && t == 0) mbar_arrive(qempty(qb));
+        }
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1;
@@ -697,14 +702,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
   if (!first) pdl_wait();
 }
 
-// One block per query row (token, query head): the partials of the prefix and
-// of the sequence's own keys, spread over the block's warps, weighted by
-// 2^(lse - largest lse) and added up.
+// A query row (token, query head) per W warps, 8 / W rows per block: the
+// partials of the prefix and of the sequence's own keys, spread over the row's
+// warps, weighted by 2^(lse - largest lse) and added up.  rows_at may hold
+// anything for rows without own keys: an entry counts where its sequence has
+// the row's token and keys, for then this call has written it.
+template <int W>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
-  __shared__ float acc_s[7][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int t = blockIdx.x, hq = blockIdx.y;
-  const int h = hq / a.G, g = hq - h * a.G;
+  __shared__ float acc_s[W > 1 ? 7 : 1][W > 1 ? 256 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = warp % W;  // of the row's warps
+  const int64_t row = (int64_t)blockIdx.x * (8 / W) + warp / W;
+  const bool live = row < (int64_t)a.T * a.hq;
   pdl_wait();
   pdl_trigger();
 
@@ -712,40 +721,27 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
   // sequence at row wrow
   int64_t p0 = 0, w0 = 0;
   int np = 0, nw = 0, pr = 0, wrow = 0;
-  if (m.pre_tiles) {
-    const int r = t * a.G + g;
+  const int t = (int)(row / a.hq), hq = (int)(row - (int64_t)t * a.hq);
+  if (live && m.own.rows_at) {
+    const int4 at = m.own.rows_at[row];
+    if (at.w >= 0 && at.w < m.own.n_seqs) {
+      const SeqInfo q = seq_info(m.own, a.T, at.w);
+      if (t >= q.q0 && t < q.q0 + q.qn && q.len > 0) {
+        w0 = at.x;
+        wrow = at.y;
+        nw = at.z;
+      }
+    }
+  }
+  if (live && m.pre_tiles) {
+    const int h = hq / a.G;
+    const int r = t * a.G + hq - h * a.G;
     const int64_t u = (int64_t)h * m.pre_blocks + r / m.pre_rows;
     const int64_t c0 = u * m.pre_tiles / m.pre_share;
     const int64_t c1 = ((u + 1) * m.pre_tiles - 1) / m.pre_share;
     p0 = u + c0;
     np = ((int)(c1 - c0) + 1) * m.pre_streams;
     pr = r % m.pre_rows;
-  }
-  {
-    int s;
-    if (m.own.q_start) {  // the last sequence that starts at or before t
-      int lo = 0, hi = m.own.n_seqs;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (m.own.q_start[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      s = lo;
-    } else {
-      s = t / m.own.max_q_len;
-    }
-    if (s < m.own.n_seqs) {
-      const SeqInfo q = seq_info(m.own, a.T, s);
-      const int j = t - q.q0;
-      if (j >= 0 && j < q.qn && q.len > 0) {
-        const int r = j * a.G + g;
-        const int64_t u = ((int64_t)s * a.hkv + h) * m.own.row_blocks + r / m.own.rows;
-        const int2 run = m.own.runs[u];
-        w0 = u + run.x;
-        nw = run.y - run.x + 1;
-        wrow = r % m.own.rows;
-      }
-    }
   }
   const int n = np + nw;
   // row of partial i of the prefix
@@ -756,19 +752,22 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
   auto lse_of = [&](int i) {
     return i < np ? m.pre_lse[pre_row(i)] : m.own.part_lse[(w0 + i - np) * m.own.rows + wrow];
   };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
+  // the first 32 partials' weights stay in the lanes
+  const float lse0 = lane < n ? lse_of(lane) : -INFINITY;
+  float M = lse0;
+  for (int i = 32 + lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float Z = M == -INFINITY ? 0.f : M;
-  float W = 0.f;
-  for (int i = lane; i < n; i += 32) W += exp2f(lse_of(i) - Z);
-  W = warp_sum(W);
+  const float wt0 = lane < n ? exp2f(lse0 - Z) : 0.f;
+  float sum = wt0;
+  for (int i = 32 + lane; i < n; i += 32) sum += exp2f(lse_of(i) - Z);
+  sum = warp_sum(sum);
 
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 4
-  for (int i = warp; i < n; i += warps) {
-    const float w = exp2f(lse_of(i) - Z);
+  for (int i = part; i < n; i += W) {
+    const float w = i < 32 ? __shfl_sync(0xffffffffu, wt0, i) : exp2f(lse_of(i) - Z);
     if (w == 0.f) continue;  // (a partial that saw nothing has no output)
     const float* o = i < np ? m.pre_o + pre_row(i) * a.D
                             : m.own.part_o + ((w0 + i - np) * m.own.rows + wrow) * a.D;
@@ -782,23 +781,29 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
         acc[k].w = fmaf(w, v.w, acc[k].w);
       }
   }
-  if (warp > 0) {
+  if (W > 1) {
+    // row r's warp `part` (from 1 on) leaves its sums for its first warp
+    const int at = warp / W * (W - 1) + part - 1;
+    if (part > 0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      *reinterpret_cast<float4*>(&acc_s[warp - 1][k * 128 + lane * 4]) = acc[k];
-  }
-  __syncthreads();
-  if (warp > 0) return;
-  for (int w = 0; w < warps - 1; ++w)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][k * 128 + lane * 4]);
-      acc[k].x += v.x;
-      acc[k].y += v.y;
-      acc[k].z += v.z;
-      acc[k].w += v.w;
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<float4*>(&acc_s[W > 1 ? at : 0][k * 128 + lane * 4]) = acc[k];
     }
-  const float inv = W == 0.f ? 0.f : 1.f / W;
+    __syncthreads();
+    if (part > 0) return;
+    for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(
+            &acc_s[W > 1 ? warp / W * (W - 1) + w : 0][k * 128 + lane * 4]);
+        acc[k].x += v.x;
+        acc[k].y += v.y;
+        acc[k].z += v.z;
+        acc[k].w += v.w;
+      }
+  }
+  if (!live) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* out = static_cast<uint16_t*>(m.out) + (int64_t)t * m.out_tok + (int64_t)hq * m.out_head;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
@@ -806,8 +811,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
       *reinterpret_cast<uint2*>(out + k * 128 + lane * 4) =
           make_uint2(pack16(acc[k].x * inv, acc[k].y * inv, a.f16),
                      pack16(acc[k].z * inv, acc[k].w * inv, a.f16));
-  if (m.lse && lane == 0)
-    m.lse[(int64_t)t * a.hq + hq] = W == 0.f ? -INFINITY : (M + log2f(W)) * 0.6931471805599453f;
+  if (m.lse && lane == 0) m.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int DP, int WR, bool F16>
@@ -857,14 +861,18 @@ cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& set, const CUtens
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s) {
   prof_begin(K_ATTN_MERGE, s);
-  // warps for the rows' partials: the prefix's are known here, a sequence's
-  // own lengths only on the device
+  // warps for a row's partials: the prefix's are known here, a sequence's own
+  // lengths only on the device
   int n = 1;
   if (m.pre_tiles) n += (m.pre_tiles / m.pre_share + 2) * m.pre_streams;
-  int warps = 1;
-  while (warps < 8 && warps * 4 < n) warps *= 2;
-  const cudaError_t e = launch_pdl(attn_merge_kernel, dim3((unsigned)a.T, (unsigned)a.hq),
-                                   dim3(32 * warps), 0, s, a, m);
+  const int64_t rows = (int64_t)a.T * a.hq;
+  auto launch = [&](auto kern, int w) {
+    const int per = 8 / w;
+    return launch_pdl(kern, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, m);
+  };
+  const cudaError_t e = n <= 8    ? launch(attn_merge_kernel<1>, 1)
+                        : n <= 32 ? launch(attn_merge_kernel<4>, 4)
+                                  : launch(attn_merge_kernel<8>, 8);
   prof_end(K_ATTN_MERGE, s);
   return e;
 }

@@ -65,7 +65,8 @@ struct AttnSet {
   int grid;                // CTAs; at most one per tile
   float* part_o;           // [units + grid][rows][D] normalised partial outputs
   float* part_lse;         // [units + grid][rows] log2 of their softmax sums
-  int2* runs;              // [units] first and last CTA of a unit (own pages)
+  int4* rows_at;           // [T][hq] (own pages) where a row's partials lie: the first
+                           // partial, the row in it, their number, the sequence
 };
 
 struct AttnArgs {
@@ -96,7 +97,7 @@ cudaError_t launch_attn_prefix_tc(const AttnArgs& a, const TcArgs& p, const CUte
                                   const CUtensorMap& mv, cudaStream_t s);
 
 struct MergeArgs {
-  AttnSet own;
+  AttnSet own;  // (rows_at NULL: no own keys)
   // the prefix's partials: key tiles of a unit and of a CTA (0: no prefix);
   // row blocks of a KV head and their rows; rows of a partial, and partials
   // of one row in it, 128 rows apart (two where streams took alternate tiles)
@@ -118,6 +119,36 @@ cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& set, const CUtens
                              const CUtensorMap& mv, bool first, cudaStream_t s);
 // Their merge into out and lse.
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s);
+
+// ---------------------------------------------------------------- copies, waits, 2^x
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tm), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+// Bounded wait of a whole warp, each lane on its own barrier: at most 2^24
+// tries, each of which suspends the thread for a short time of the hardware's
+// choosing; on giving up it sets *abort and the TIMEOUT status.  The loop is a
+// handful of instructions on purpose: with a time limit in line (%globaltimer,
+// a second vote) each wait cost some 250 cycles even where it passed at once,
+// and plain polling took issue slots from the warps that compute.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* status) {
+  bool ok = false;
+  for (uint32_t n = 0; n < 1u << 24 && !ok; ++n) ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  *abort = 1;
+  set_status(status, LILY_STATUS_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ---------------------------------------------------------------- 16-bit elements
 __device__ __forceinline__ float lo16_f32(uint32_t w, bool f16) {

@@ -80,7 +80,7 @@ struct Plan {
   AttnSet pre, own;  // pre: not on the tensor-core kernel
   TcArgs ptc;
   int64_t pre_units, pre_total, own_most;  // units; tiles; tiles at most
-  size_t pre_o, pre_lse, own_o, own_lse, runs, bytes;
+  size_t pre_o, pre_lse, own_o, own_lse, rows_at, bytes;
 };
 
 void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G) {
@@ -134,11 +134,12 @@ bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   p.own.causal = max_q_len > 1;
   const int64_t units = (int64_t)d.n_seqs * c.n_kv_heads * p.own.row_blocks;
   if (units > INT_MAX / 2) return false;
+  if (units * ((d.max_seq_len + kAttnTile - 1) / kAttnTile) > INT_MAX / 2) return false;
   p.own_most = units * ((d.max_seq_len + kAttnTile - 1) / kAttnTile);
   if (d.max_seq_len) {
     partials(units, p.own_most, kAttnMaxGrid, p.own.rows, p.own_o, p.own_lse);
-    p.runs = off;
-    off += up256((size_t)units * 8);
+    p.rows_at = off;
+    off += up256((size_t)d.n_tokens * d.n_q_heads * 16);
   }
   p.bytes = off;
   return true;
@@ -377,21 +378,19 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     if (e != cudaSuccess) return LILY_ERR_CUDA;
     first = false;
   }
-  m.own = p.own;
-  m.own.q_start = q_start;
-  m.own.lens = seq_lens;
   if (d.max_seq_len) {
-    AttnSet& o = m.own;
+    AttnSet& o = p.own;
+    o.q_start = q_start;
+    o.lens = seq_lens;
     o.table = block_table;
     o.table_stride = d.table_stride;
     o.part_o = reinterpret_cast<float*>(base + p.own_o);
     o.part_lse = reinterpret_cast<float*>(base + p.own_lse);
-    o.runs = reinterpret_cast<int2*>(base + p.runs);
+    o.rows_at = reinterpret_cast<int4*>(base + p.rows_at);
     o.grid = (int)(p.own_most < grid ? p.own_most : grid);
+    m.own = o;
     if (!maps(kAttnTile, kAttnTile)) return LILY_ERR_CUDA;
     if (launch_attn_keys(a, o, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
-  } else {
-    m.own.n_seqs = 0;
   }
   return rc_of(launch_attn_merge(a, m, s));
 }

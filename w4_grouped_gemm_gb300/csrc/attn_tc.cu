@@ -55,19 +55,6 @@ struct Tc {
   static_assert(kO + kGroups * DP <= 512, "tensor memory");
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,
-                                            int c2, int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(tm), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Shared-memory descriptors with the 128-byte swizzle, as a constant high word
 // (stride offset 1024 between groups of 8 rows, version, swizzle) and a low
 // word (address, leading offset) that advances by adding bytes / 16.
@@ -122,21 +109,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// Bounded wait of a whole warp, each lane on its own barrier: 2^22 polls of at
-// least 50 cycles; on giving up it sets *abort and the TIMEOUT status.  The loop
-// is a handful of instructions on purpose: with the time limit of the other
-// kernels in line (%globaltimer, a second vote) each wait cost some 250 cycles,
-// even where it passed at once.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
-  bool ok = false;
-  for (uint32_t n = 0; n < 1u << 24 && !ok; ++n) ok = mbar_try_wait(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  *abort = 1;
-  set_status(status, LILY_STATUS_TIMEOUT);
-  return false;
-}
-
 // Keeps every use of r after the point (the wait of the load that filled it).
 __device__ __forceinline__ void tie(uint32_t (&r)[32]) {
 #pragma unroll
@@ -509,7 +481,6 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
     if (C::kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int g = (warp - kCtrlWarps) >> 2;          // stream
     const int quad = warp & 3, row = quad * 32 + lane;
-    const int tid = threadIdx.x - 32 * kCtrlWarps - 128 * g;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // tensor memory lane field
     const float c = a.scale_log2;
     uint32_t s_par = 0;  // parity of buffer b's scores: bit b
@@ -520,17 +491,32 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       const int row0 = run.unit % p.row_blocks * p.block_rows + (paired ? g * 128 : 0);
       const int nrows = min(128, rows_all - row0);  // may be 0 or less
       // rows of Q, 16 bytes at a time, swizzled; zeros past the rows and past D
-      for (int x = tid; x < 128 * blocks * 8; x += 128) {
-        const int r = x / (blocks * 8), e = x - r * blocks * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < nrows && e * 8 < a.D) {
+      // (a warp brings its own 32 rows, eight per thread, whose loads of a block
+      // are in flight together)
+      {
+        const int e = lane & 7;
+        int64_t at[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = quad * 32 + i * 4 + (lane >> 3);
           const int rr = row0 + r, j = rr / a.G, gg = rr - j * a.G;
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                              (int64_t)j * a.q_tok +
-                                              (int64_t)(h * a.G + gg) * a.q_head + e * 8);
+          at[i] = r < nrows ? (int64_t)j * a.q_tok + (int64_t)(h * a.G + gg) * a.q_head : -1;
         }
-        *reinterpret_cast<uint4*>(smem + g * C::kQTile + (e >> 3) * 128 * 128 + r * 128 +
-                                  (((e & 7) ^ (r & 7)) << 4)) = v;
+        for (int k = 0; k < blocks; ++k) {
+          const int col = k * 64 + e * 8;
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = at[i] >= 0 && col < a.D
+                       ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i] + col)
+                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = quad * 32 + i * 4 + (lane >> 3);
+            *reinterpret_cast<uint4*>(smem + g * C::kQTile + k * 128 * 128 + r * 128 +
+                                      ((e ^ (r & 7)) << 4)) = v[i];
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -663,31 +649,43 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       }
       if (!ok) break;
 
-      // the segment's partial: O / l and the log of its weight
+      // the unit's partial: O / l and the log of its weight
       if (any) {
         ok = wait_warp(o_full(g), (o_cnt - 1) & 1, &abort_s, a.status);
         if (!ok) break;
         tc_fence_after();
       }
-      const int64_t slot_row =
-          ((int64_t)run.unit + blockIdx.x) * (128 * C::kGroups) + 128 * g + row;
+      const int64_t slot0 =
+          ((int64_t)run.unit + blockIdx.x) * (128 * C::kGroups) + 128 * g + quad * 32;
+      const int64_t slot_row = slot0 + lane;
       const bool live = row < nrows;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float* out = p.part_o + slot_row * a.D;
-      if (any)
+      // 32 columns at a time through the first block of the warp's own rows of Q
+      // (whose last product is done), so that rows leave in whole 128-byte lines
+      if (any) {
+        uint8_t* stage = smem + g * C::kQTile + quad * 4096;
         for (int i = 0; i < blocks * 2; ++i) {
           uint32_t o[32];
           tmem_ld32(tmem + lanes + C::kO + DP * g + 32 * i, o);
           tmem_ld_wait();
           tie(o);
-          if (live)
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              if (32 * i + j < a.D)
-                *reinterpret_cast<float4*>(out + 32 * i + j) = make_float4(
-                    __uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
-                    __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(
+                __uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
+          __syncwarp();
+          const int piece = lane & 7, col = 32 * i + 4 * piece;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = j * 4 + (lane >> 3);
+            if (quad * 32 + r < nrows && col < a.D)
+              *reinterpret_cast<float4*>(p.part_o + (slot0 + r) * a.D + col) =
+                  *reinterpret_cast<const float4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+          }
+          __syncwarp();
         }
+      }
       tc_fence_before();
       if (live) p.part_lse[slot_row] = l == 0.f ? -INFINITY : z + log2f(l);
     }
