@@ -101,7 +101,7 @@ typedef struct {
  * rotary_dim   leading dimensions of a head that rotate: even, 0 to head_dim
  * style        0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i + 1)
  * strides      elements, per token and per head, of q, k, v and q_out:
- *              multiples of 8
+ *              multiples of 8, below 2^31
  */
 typedef struct {
   int32_t T, n_q_heads, rotary_dim, style;

@@ -108,7 +108,7 @@ def test_rope_refusals(L):
     for bad in (dict(T=0), dict(n_q_heads=-1), dict(rotary_dim=-2)):
         assert _rope(L, _with(ok, **bad)) == ARG, bad
     for bad in (dict(rotary_dim=63), dict(rotary_dim=130), dict(style=2),
-                dict(q_token_stride=2052), dict(k_head_stride=-8), dict(v_token_stride=1 << 40),
+                dict(q_token_stride=2052), dict(k_head_stride=-8), dict(v_token_stride=1 << 40), dict(q_head_stride=1 << 31),
                 dict(qo_head_stride=4)):
         assert _rope(L, _with(ok, **bad)) == SHAPE, bad
     assert _rope(L, ok, n=255) == SMALL

@@ -36,7 +36,7 @@ struct RopeArgs {
   const int32_t* pos;
   const int64_t* slots;
   const double* inv_freq;
-  int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head;
+  int32_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head;
   int64_t c_page, c_head, c_tok, n_slots;
   int T, hq, hkv, D, rot, style, page_shift, dtype;
   uint32_t* status;

@@ -234,7 +234,8 @@ int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache
                              d.v_token_stride, d.v_head_stride, d.qo_token_stride, d.qo_head_stride};
   for (int i = 0; i < 8; ++i) {
     const bool used = i < 2 || i >= 6 ? q != nullptr : k != nullptr;
-    if (used && !head_stride_ok(strides[i])) return LILY_ERR_UNSUPPORTED_SHAPE;
+    if (used && (!head_stride_ok(strides[i]) || strides[i] > INT_MAX))
+      return LILY_ERR_UNSUPPORTED_SHAPE;
   }
   const void* ptrs[] = {q, k, v, q_out, workspace};
   for (const void* p : ptrs)
@@ -256,12 +257,12 @@ int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache
   a.inv_freq = inv_freq;
   a.q_tok = d.q_token_stride;
   a.q_head = d.q_head_stride;
-  a.k_tok = d.k_token_stride;
-  a.k_head = d.k_head_stride;
-  a.v_tok = d.v_token_stride;
-  a.v_head = d.v_head_stride;
-  a.qo_tok = d.qo_token_stride;
-  a.qo_head = d.qo_head_stride;
+  a.k_tok = (int32_t)d.k_token_stride;
+  a.k_head = (int32_t)d.k_head_stride;
+  a.v_tok = (int32_t)d.v_token_stride;
+  a.v_head = (int32_t)d.v_head_stride;
+  a.qo_tok = (int32_t)d.qo_token_stride;
+  a.qo_head = (int32_t)d.qo_head_stride;
   a.c_page = cache->page_stride;
   a.c_head = cache->head_stride;
   a.c_tok = cache->token_stride;

@@ -32,21 +32,36 @@ __device__ __forceinline__ void load_raw8(Raw8& r, const void* p, int64_t i, int
   }
 }
 
+// (one branch per eight elements, not a choice per element)
 __device__ __forceinline__ void unpack8(const Raw8& r, int type, float (&v)[8]) {
   if (type == LILY_DTYPE_F32) {
     v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
     v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
     v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
     v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
-  } else {
-    const bool h = type == LILY_DTYPE_F16;
-    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    return;
+  }
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  if (type == LILY_DTYPE_F16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = lo16_f32(w[j], h);
-      v[2 * j + 1] = hi16_f32(w[j], h);
+      v[2 * j] = lo16_f32(w[j], true);
+      v[2 * j + 1] = hi16_f32(w[j], true);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = lo16_f32(w[j], false);
+      v[2 * j + 1] = hi16_f32(w[j], false);
     }
   }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool f16) {
+  if (f16)
+    return make_uint4(pack16(v[0], v[1], true), pack16(v[2], v[3], true), pack16(v[4], v[5], true),
+                      pack16(v[6], v[7], true));
+  return make_uint4(pack16(v[0], v[1], false), pack16(v[2], v[3], false),
+                    pack16(v[4], v[5], false), pack16(v[6], v[7], false));
 }
 
 __device__ __forceinline__ float load1(const void* p, int64_t i, int type) {
@@ -84,12 +99,17 @@ __device__ __forceinline__ float row_reduce(float v, float* tmp) {
 // A row on WPR warps, C chunks of eight elements per thread.  VEC: chunk c of
 // thread t covers columns 8 (c*threads + t) .. +7; else its elements are the
 // columns (8c + e)*threads + t, one at a time (any alignment).
-template <int WPR, int C, bool VEC>
+// XT, RT, OT: element types known when compiling, -1: asked at run time (OT 0:
+// one of the 16-bit types).  Asked at run time they cost half of the issue
+// slots, which then bound the kernel (16384 rows of 4096 into 8 bits: 93 us).
+template <int WPR, int C, bool VEC, int XT, int RT, int OT>
 __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
     add_rmsnorm_kernel(const NormArgs a) {
   constexpr int kTPR = WPR * 32;
   constexpr int kThreads = kTPR > 256 ? kTPR : 256;
   constexpr int kRows = kThreads / kTPR;
+  const int xt = XT >= 0 ? XT : a.xt, rt = RT >= 0 ? RT : a.rt;
+  const bool bits8 = OT >= 0 ? OT == LILY_DTYPE_E4M3 : a.ot == LILY_DTYPE_E4M3;
   __shared__ float tmp[2][kThreads / 32];
   __shared__ uint32_t gmax[VEC ? 1 : kRows][VEC ? 1 : 256];  // element-wise groups: bits of the maxima
 
@@ -109,16 +129,16 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (live && col(c, 0) < a.d) {
-        load_raw8(rx[c], a.x, xi + col(c, 0), a.xt);
-        if (a.res) load_raw8(rr[c], a.res, ri + col(c, 0), a.rt);
+        load_raw8(rx[c], a.x, xi + col(c, 0), xt);
+        if (a.res) load_raw8(rr[c], a.res, ri + col(c, 0), rt);
       }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (live && col(c, 0) < a.d) {
-        unpack8(rx[c], a.xt, r[c]);
+        unpack8(rx[c], xt, r[c]);
         if (a.res) {
           float v[8];
-          unpack8(rr[c], a.rt, v);
+          unpack8(rr[c], rt, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) r[c][e] += v[e];
         }
@@ -132,13 +152,13 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        r[c][e] = live && col(c, e) < a.d ? load1(a.x, xi + col(c, e), a.xt) : 0.f;
+        r[c][e] = live && col(c, e) < a.d ? load1(a.x, xi + col(c, e), xt) : 0.f;
     if (a.res)
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (live && col(c, e) < a.d) r[c][e] += load1(a.res, ri + col(c, e), a.rt);
+          if (live && col(c, e) < a.d) r[c][e] += load1(a.res, ri + col(c, e), rt);
   }
 
   float ss = 0.f;
@@ -156,49 +176,48 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
       if (!(live && col(c, 0) < a.d)) continue;
       if (a.res_out) {
         const int64_t o = row * a.res_out_stride + col(c, 0);
-        if (a.rt == LILY_DTYPE_F32) {
+        if (rt == LILY_DTYPE_F32) {
           float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + o);
           p[0] = make_float4(r[c][0], r[c][1], r[c][2], r[c][3]);
           p[1] = make_float4(r[c][4], r[c][5], r[c][6], r[c][7]);
         } else {
-          const bool h = a.rt == LILY_DTYPE_F16;
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + o) =
-              make_uint4(pack16(r[c][0], r[c][1], h), pack16(r[c][2], r[c][3], h),
-                         pack16(r[c][4], r[c][5], h), pack16(r[c][6], r[c][7], h));
+              pack8(r[c], rt == LILY_DTYPE_F16);
         }
       }
-      float w[8];
       if (a.w) {
+        float w[8];
         Raw8 rw;
         load_raw8(rw, a.w, col(c, 0), a.wt);
         unpack8(rw, a.wt, w);
-      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[c][e] *= a.w ? rstd * w[e] : rstd;
+        for (int e = 0; e < 8; ++e) r[c][e] *= rstd * w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[c][e] *= rstd;
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (!(live && col(c, e) < a.d)) continue;
         if (a.res_out) {
           const int64_t o = row * a.res_out_stride + col(c, e);
-          if (a.rt == LILY_DTYPE_F32) static_cast<float*>(a.res_out)[o] = r[c][e];
-          else static_cast<uint16_t*>(a.res_out)[o] = pack1(r[c][e], a.rt == LILY_DTYPE_F16);
+          if (rt == LILY_DTYPE_F32) static_cast<float*>(a.res_out)[o] = r[c][e];
+          else static_cast<uint16_t*>(a.res_out)[o] = pack1(r[c][e], rt == LILY_DTYPE_F16);
         }
         r[c][e] *= a.w ? rstd * load1(a.w, col(c, e), a.wt) : rstd;
       }
     }
   }
 
-  if (a.ot != LILY_DTYPE_E4M3) {
+  if (!bits8) {
     const bool h = a.ot == LILY_DTYPE_F16;
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_stride;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (VEC) {
         if (live && col(c, 0) < a.d)
-          *reinterpret_cast<uint4*>(out + col(c, 0)) =
-              make_uint4(pack16(r[c][0], r[c][1], h), pack16(r[c][2], r[c][3], h),
-                         pack16(r[c][4], r[c][5], h), pack16(r[c][6], r[c][7], h));
+          *reinterpret_cast<uint4*>(out + col(c, 0)) = pack8(r[c], h);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -257,46 +276,66 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 
   float* sc = a.scales + row * n_groups;
   uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
-  // 1 / s while it is a normal number; below, divide (n / s is at most 448)
-  auto inverse = [](float s) { return s > 1e-30f ? 1.f / s : 0.f; };
-  auto scaled = [](float n, float s, float inv) {
-    return inv != 0.f || !(s > 0.f) ? n * inv : n / s;
-  };
-  if (per_row && t == 0) sc[0] = __uint_as_float(VEC ? m[0] : m[0]) / 448.f;
+  // n / s as n * (448 / max); where that would not be a normal number, divided
+  // (the last bits of the quotient are lost in e4m3's rounding, and the largest
+  // value still lands on 448)
+  constexpr float kTiny = 1e-30f, kStep = 1.f / 448.f;
+  if (per_row && t == 0) sc[0] = __uint_as_float(m[0]) * kStep;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (VEC) {
       if (col(c, 0) >= a.d) continue;
-      const float s = __uint_as_float(m[c]) / 448.f, inv = s == s ? inverse(s) : s;
-      if (!per_row && (col(c, 0) % a.group) == 0) sc[col(c, 0) / a.group] = s;
-      float q[8];
+      const float top = __uint_as_float(m[c]), s = top * kStep;
+      if (!per_row && (col(c, 0) & (a.group - 1)) == 0) sc[col(c, 0) / a.group] = s;
+      if (s > 0.f && s < kTiny) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = scaled(r[c][e], s, inv);
+        for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] / s;
+      } else {
+        const float inv = top == 0.f ? 0.f : __fdividef(448.f, top);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[c][e] *= inv;
+      }
       uint2 o;
-      o.x = e4m3x2(q[0], q[1]) | (uint32_t)e4m3x2(q[2], q[3]) << 16;
-      o.y = e4m3x2(q[4], q[5]) | (uint32_t)e4m3x2(q[6], q[7]) << 16;
+      o.x = e4m3x2(r[c][0], r[c][1]) | (uint32_t)e4m3x2(r[c][2], r[c][3]) << 16;
+      o.y = e4m3x2(r[c][4], r[c][5]) | (uint32_t)e4m3x2(r[c][6], r[c][7]) << 16;
       *reinterpret_cast<uint2*>(out + col(c, 0)) = o;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = col(c, e);
         if (i >= a.d) continue;
-        const float s = __uint_as_float(per_row ? m[0] : gmax[sub][i / a.group]) / 448.f;
+        const float s = __uint_as_float(per_row ? m[0] : gmax[sub][i / a.group]) * kStep;
         if (!per_row && i % a.group == 0) sc[i / a.group] = s;
-        const float inv = s == s ? inverse(s) : s;
-        out[i] = (uint8_t)e4m3x2(scaled(r[c][e], s, inv), 0.f);
+        const float q = s == 0.f ? 0.f : r[c][e] / s;
+        out[i] = (uint8_t)e4m3x2(q, 0.f);
       }
     }
   }
 }
 
-template <int WPR, int C>
-cudaError_t launch_as(const NormArgs& a, bool vec, cudaStream_t s) {
+template <int WPR, int C, int XT, int RT, int OT>
+cudaError_t launch_types(const NormArgs& a, bool vec, cudaStream_t s) {
   constexpr int kThreads = WPR * 32 > 256 ? WPR * 32 : 256;
   constexpr int kRows = kThreads / (WPR * 32);
   const unsigned grid = (unsigned)(((int64_t)a.T + kRows - 1) / kRows);
-  return vec ? launch_pdl(add_rmsnorm_kernel<WPR, C, true>, dim3(grid), dim3(kThreads), 0, s, a)
-             : launch_pdl(add_rmsnorm_kernel<WPR, C, false>, dim3(grid), dim3(kThreads), 0, s, a);
+  if (XT < 0 && !vec)
+    return launch_pdl(add_rmsnorm_kernel<WPR, C, false, -1, -1, -1>, dim3(grid), dim3(kThreads), 0, s, a);
+  return launch_pdl(add_rmsnorm_kernel<WPR, C, true, XT, RT, OT>, dim3(grid), dim3(kThreads), 0, s, a);
+}
+// The types of one kind throughout, with an fp32 residual or without one, are
+// compiled in; other mixtures, and rows of any alignment, ask at run time.
+template <int WPR, int C>
+cudaError_t launch_as(const NormArgs& a, bool vec, cudaStream_t s) {
+  constexpr int B = LILY_DTYPE_BF16, H = LILY_DTYPE_F16, F = LILY_DTYPE_F32, Q = LILY_DTYPE_E4M3;
+  const bool q = a.ot == Q;
+  if (vec && (a.rt == F || a.rt == a.xt)) {
+    if (a.xt == B && a.rt == B) return q ? launch_types<WPR, C, B, B, Q>(a, vec, s) : launch_types<WPR, C, B, B, 0>(a, vec, s);
+    if (a.xt == B) return q ? launch_types<WPR, C, B, F, Q>(a, vec, s) : launch_types<WPR, C, B, F, 0>(a, vec, s);
+    if (a.xt == H && a.rt == H) return q ? launch_types<WPR, C, H, H, Q>(a, vec, s) : launch_types<WPR, C, H, H, 0>(a, vec, s);
+    if (a.xt == H) return q ? launch_types<WPR, C, H, F, Q>(a, vec, s) : launch_types<WPR, C, H, F, 0>(a, vec, s);
+    return q ? launch_types<WPR, C, F, F, Q>(a, vec, s) : launch_types<WPR, C, F, F, 0>(a, vec, s);
+  }
+  return launch_types<WPR, C, -1, -1, -1>(a, vec, s);
 }
 
 }  // namespace
@@ -306,11 +345,9 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, bool vec, cudaStream_t s) {
   const int n8 = (a.d + 7) / 8;  // chunks of a row
   cudaError_t e;
   if (n8 <= 32) e = launch_as<1, 1>(a, vec, s);
-  else if (n8 <= 64) e = launch_as<2, 1>(a, vec, s);
   else if (n8 <= 128) e = launch_as<4, 1>(a, vec, s);
   else if (n8 <= 256) e = launch_as<8, 1>(a, vec, s);
-  else if (n8 <= 512) e = launch_as<16, 1>(a, vec, s);
-  else if (n8 <= 1024) e = launch_as<16, 2>(a, vec, s);
+  else if (n8 <= 512) e = launch_as<8, 2>(a, vec, s);
   else e = launch_as<16, 4>(a, vec, s);
   prof_end(K_ATTN_NORM, s);
   return e;
