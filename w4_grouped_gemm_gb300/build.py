@@ -18,7 +18,8 @@ INCLUDE = PKG.parent / "include"
 BUILD = PKG / "_build"
 LIB = PKG / "liblily_moe.so"
 SOURCES = ["api.cu", "route.cu", "gemm.cu", "decode.cu", "misc.cu", "static_ws.cu",
-           "attn_api.cu", "attn_norm.cu", "attn_rope.cu", "attn.cu", "attn_tc.cu"]
+           "attn_api.cu", "attn_norm.cu", "attn_rope.cu", "attn.cu",
+           "attn_keys_bf16.cu", "attn_keys_f16.cu", "attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]

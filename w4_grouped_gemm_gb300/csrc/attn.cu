@@ -1,727 +1,53 @@
-// attn.cu -- attention over a paged cache for a batch that shares a prefix:
-// partial outputs over runs of keys, and their merge (lily_attn_shared_prefix).
-//
-//   out = sum_k softmax_k(scale q.k) v_k.  Over any part of the keys, with
-//   m = max s, l = sum 2^(c (s - m)), o = sum 2^(c (s - m)) v / l, c = scale log2(e),
-//   the part's weight is 2^(c m + log2 l); parts add up with those weights.
-//
-// The shared prefix is one "sequence" whose query rows are the whole batch's,
-// so its keys and values are read once for all; each sequence's own pages are
-// a sequence of few rows (its new tokens times the query heads per KV head).
-// Both run here as a set of units (AttnSet): the units' 64-key tiles form one
-// list that the CTAs share out evenly, whatever the lengths, and a unit cut
-// between CTAs leaves one partial per CTA for the merge.  Few rows and long
-// lengths so fill the GPU as well as many rows and short ones.
-//
-// Per CTA one producer warp and four warps of mma.sync (16 rows each).  Up to
-// 64 rows meet each key, so a byte of K or V brings at most 64 flop: HBM
-// bounds these units, not the tensor cores, and mma.sync keeps the softmax in
-// registers.  The producer brings K, V (TMA, one box per page and 64
-// dimensions) and the rows of Q into a ring of stages; the warps split a
-// tile's keys when rows are few (16 rows: 16 keys each; 64 rows: a row block
-// each).  Two CTAs per SM (heads of up to 128) hide one's softmax and merges
-// behind the other's loads.
+// attn.cu -- the merge of attention's partial outputs, and the launches of
+// lily_attn_shared_prefix's kernels (attn_keys.cuh, attn_tc.cu).
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace lily {
 namespace {
 
-constexpr int kWarps = 4;                       // compute warps
-constexpr int kThreads = 32 * (kWarps + 1);     // and the producer
-constexpr int kTile = kAttnTile;
-
-__host__ __device__ constexpr int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-
-// DP: head dimension rounded up to 64, 128 or 256 (the rest reads as zero);
-// WR: blocks of 16 rows.
-template <int DP, int WR>
-struct Cfg {
-  static constexpr int kRows = 16 * WR;
-  static constexpr int kWK = kWarps / WR;        // warps that split a tile's keys
-  static constexpr int kKeys = kTile / kWK;      // keys of a warp
-  static constexpr int kOcc = DP <= 128 ? 2 : 1;
-  static constexpr int kStages = DP == 64 ? 6 : 3;
-  static constexpr int kHalfBytes = kTile * 128;             // 64 keys x 64 dimensions
-  static constexpr int kTileBytes = kHalfBytes * (DP / 64);  // K or V of a tile
-  static constexpr int kStageBytes = 2 * kTileBytes;
-  // Q: up to 128 dimensions live in registers during a unit, so one buffer
-  // is free again at once; 256 stay in shared memory (rows padded by 16 bytes)
-  static constexpr bool kQRegs = DP <= 128;
-  static constexpr int kQPitch = kQRegs ? DP * 2 : DP * 2 + 16;
-  static constexpr int kQBufs = kQRegs || WR > 1 ? 1 : 2;
-  static constexpr int kQBytes = kRows * kQPitch;
-  // columns of O that the warps of a row block exchange at a time
-  static constexpr int kRedCols = WR == 1 ? 32 : 16;
-  static constexpr int kRedPitch = kRedCols + 4;
-  static constexpr int kRedBytes = kWK > 1 ? kWarps * 16 * kRedPitch * 4 : 0;
-  static constexpr int kQOff = kStages * kStageBytes;
-  static constexpr int kRedOff = kQOff + kQBufs * kQBytes;
-  static constexpr int kBytes = kRedOff + kRedBytes;
-};
-
-struct alignas(16) Desc {
-  int part, head, q0, row0;   // partial index (-1: no more); KV head; first token; first row
-  int nrows, qn, len, key0;   // rows; tokens and keys of the sequence; first key
-  int tiles, pad[3];
-};
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  if (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// Byte offset of 16-byte piece c (0..7) of row r in a tile of 128-byte rows
-// with the 128-byte swizzle (tile base 1024-byte aligned).
-__device__ __forceinline__ uint32_t swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-
-// A sequence's query tokens and own keys, held inside the call's bounds.
-struct SeqInfo {
-  int q0, qn, len;
-  bool bad;
-};
-__device__ __forceinline__ SeqInfo seq_info(const AttnSet& s, int T, int i) {
-  SeqInfo r;
-  r.bad = false;
-  int q1;
-  if (s.q_start) {
-    r.q0 = s.q_start[i];
-    q1 = s.q_start[i + 1];
-  } else {
-    r.q0 = i * s.max_q_len;
-    q1 = r.q0 + s.max_q_len;
-  }
-  if (r.q0 < 0 || r.q0 > T || q1 < r.q0 || q1 > T || q1 - r.q0 > s.max_q_len) {
-    r.bad = true;
-    r.q0 = min(max(r.q0, 0), T);
-    q1 = min(max(q1, r.q0), min(T, r.q0 + s.max_q_len));
-  }
-  r.qn = q1 - r.q0;
-  r.len = s.lens ? s.lens[i] : s.max_len;
-  if (r.len < 0 || r.len > s.max_len) {
-    r.bad = true;
-    r.len = min(max(r.len, 0), s.max_len);
-  }
-  return r;
-}
-// Units and tiles of a sequence: row blocks per KV head, and tiles per unit.
-__device__ __forceinline__ int blocks_of(const AttnSet& s, int G, int qn) {
-  return (qn * G + s.rows - 1) / s.rows;
-}
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
-
-// Partials of one set.  first: this launch follows the call's predecessor and
-// waits for it; else it follows the other set's launch, which has waited, and
-// only ends after it (so that the merge, which waits for this launch, sees both).
-template <int DP, int WR, bool F16>
-__global__ void __launch_bounds__(kThreads, Cfg<DP, WR>::kOcc)
-    attn_keys_kernel(const AttnArgs a, const AttnSet set, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, bool first) {
-  using C = Cfg<DP, WR>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * C::kQBufs];
-  __shared__ Desc desc[C::kQBufs];
-  __shared__ unsigned long long mask_s[C::kStages];  // valid keys of a stage
-  __shared__ int total_s[kWarps + 1];
-  __shared__ float red_z[kWarps][16], red_l[kWarps][16];
-  __shared__ int abort_s;
-  __shared__ int dead_s[2];  // compute warps agree at each unit whether to go on
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem);
-  const uint32_t bar0 = smem_u32(bars);
-  auto full = [&](int i) { return bar0 + 8 * i; };
-  auto empty = [&](int i) { return bar0 + 8 * (C::kStages + i); };
-  auto qfull = [&](int i) { return bar0 + 8 * (2 * C::kStages + i); };
-  auto qempty = [&](int i) { return bar0 + 8 * (2 * C::kStages + C::kQBufs + i); };
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), kWarps);
-    }
-    for (int i = 0; i < C::kQBufs; ++i) {
-      mbar_init(qfull(i), 1);
-      mbar_init(qempty(i), kWarps);
-    }
-    fence_mbar_init();
-    abort_s = 0;
-    dead_s[0] = dead_s[1] = 0;
-    prefetch_tensormap(&mk);
-    prefetch_tensormap(&mv);
-  }
-  // Q rows start as zeros: dimensions past D are never written and meet K's
-  // zero fill, rows past a unit's last hold numbers
-  for (int i = threadIdx.x; i < C::kQBufs * C::kQBytes / 16; i += kThreads)
-    reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0, 0, 0, 0);
-  // and blocks of 64 dimensions past D, which no copy writes
-  const int halves = (a.D + 63) / 64;
-  if (halves < DP / 64)
-    for (int i = threadIdx.x; i < C::kStages * 2 * C::kTileBytes / 16; i += kThreads)
-      if (i % (C::kTileBytes / 16) >= halves * (C::kHalfBytes / 16))
-        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-
-  if (first) pdl_wait();
-  pdl_trigger();
-
-  // the set's tiles (31 bits: checked on the host), and this CTA's run of them
-  auto cost_of = [&](const SeqInfo& q) { return a.hkv * blocks_of(set, a.G, q.qn) * tiles_of(q.len); };
-  int sum = 0;
-  for (int i = threadIdx.x; i < set.n_seqs; i += kThreads) {
-    const SeqInfo q = seq_info(set, a.T, i);
-    if (q.bad && blockIdx.x == 0) set_status(a.status, LILY_STATUS_BAD_LEN);
-    sum += cost_of(q);
-  }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) total_s[warp] = sum;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w <= kWarps; ++w) total += total_s[w];
-  const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, set.min_share);
-  const int begin = (int)min((int64_t)share * blockIdx.x, (int64_t)total);
-  const int end = min(begin + share, total);
-
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer
-    // Short sequences make this warp the bottleneck, so it keeps global memory
-    // latency off its path: 32 sequences' lengths lie in the lanes, the next
-    // sequence's first pages are requested a sequence ahead.
-    int stage = 0, phase = 0, seg = 0;
-    bool ok = true;
-    uint32_t used = 0;  // stages filled at least once
-    const int ps = a.page_shift;
-    const int box_rows = min(kTile, 1 << ps);
-    const int pages_per_tile = kTile / box_rows;
-    const uint32_t box_bytes = box_rows * 128;
-    // lane l: page l / (2 halves) of a tile, K or V, half of the head
-    const int i = lane / (2 * halves), rest = lane - i * 2 * halves;
-    const bool is_v = rest >= halves;
-    const int hf = rest - (is_v ? halves : 0);
-    const uint32_t at_stage = (is_v ? C::kTileBytes : 0) + hf * C::kHalfBytes + i * box_bytes;
-
-    int at = begin;
-    int s0 = -1, s = 0;       // sequences s0 .. s0 + 31 lie in the lanes; current one
-    int s_base = 0;           // first tile of sequence s
-    SeqInfo mine = {};        // of sequence s0 + lane
-    int my_cost = 0, my_base = 0;
-    auto load32 = [&](int first_seq, int base_tile) {
-      s0 = first_seq;
-      mine = SeqInfo{};
-      if (s0 + lane < set.n_seqs) mine = seq_info(set, a.T, s0 + lane);
-      my_cost = s0 + lane < set.n_seqs ? cost_of(mine) : 0;
-      int inc = my_cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      my_base = base_tile + inc - my_cost;
-    };
-    // the sequence that holds tile t, from the current group on; false past the last
-    auto find = [&](int t) {
-      for (;;) {
-        const uint32_t in = __ballot_sync(0xffffffffu, my_cost > 0 && my_base + my_cost > t);
-        if (in) {
-          s = s0 + __ffs(in) - 1;
-          s_base = __shfl_sync(0xffffffffu, my_base, s - s0);
-          return true;
-        }
-        if (s0 + 32 >= set.n_seqs) return false;
-        load32(s0 + 32, __shfl_sync(0xffffffffu, my_base + my_cost, 31));
-      }
-    };
-    // page indices of the current sequence from page pbase on, and of the next one
-    auto first_pages = [&](int seq, int page) {
-      const int n = seq < s0 + 32 && seq < set.n_seqs ? __shfl_sync(0xffffffffu, mine.len, seq - s0) : 0;
-      const int p = page + lane;
-      return n > 0 && p <= (n - 1) >> ps ? set.table[(int64_t)seq * set.table_stride + p] : -1;
-    };
-    int pseq = -1, pbase = 0, pcache = 0, next_cache = 0;
-    if (at < end) {
-      load32(0, 0);
-      ok = find(at);
-    }
-    while (ok && at < end) {
-      SeqInfo q;
-      q.q0 = __shfl_sync(0xffffffffu, mine.q0, s - s0);
-      q.qn = __shfl_sync(0xffffffffu, mine.qn, s - s0);
-      q.len = __shfl_sync(0xffffffffu, mine.len, s - s0);
-      const int nt = tiles_of(q.len), nb = blocks_of(set, a.G, q.qn);
-      const int in_seq = (at - s_base) / nt;  // unit of the sequence
-      const int t0 = (at - s_base) - in_seq * nt;
-      const int nseg = min(nt - t0, end - at);
-      const int h = in_seq / nb, blk = in_seq - h * nb;
-      const int unit = (s * a.hkv + h) * set.row_blocks + blk;
-      const int row0 = blk * C::kRows;
-      const int nrows = min(C::kRows, q.qn * a.G - row0);
-      const int last = (q.len - 1) >> ps;
-      if (s != pseq) {
-        // a sequence's first pages came with the one before it, if it was that
-        // one's neighbour and starts here
-        const bool have = pseq >= 0 && s == pseq + 1 && t0 == 0 && s > s0;
-        pbase = (t0 * kTile) >> ps;
-        pcache = have ? next_cache : first_pages(s, pbase);
-        next_cache = first_pages(s + 1, 0);
-        pseq = s;
-      }
-
-      const int qb = seg % C::kQBufs;
-      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.status);
-      if (!ok) break;
-      if (lane == 0) {
-        Desc d;
-        d.part = unit + blockIdx.x;
-        d.head = h;
-        d.q0 = q.q0;
-        d.row0 = row0;
-        d.nrows = nrows;
-        d.qn = q.qn;
-        d.len = q.len;
-        d.key0 = t0 * kTile;
-        d.tiles = nseg;
-        desc[qb] = d;
-        mbar_arrive_expect_tx(qfull(qb), nrows * a.D * 2);
-      }
-      __syncwarp();
-      for (int r = lane; r < nrows; r += 32) {
-        const int rr = row0 + r;
-        const int j = rr / a.G, g = rr - j * a.G;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(q.q0 + j) * a.q_tok +
-                              (int64_t)(h * a.G + g) * a.q_head;
-        bulk_load(base + C::kQOff + qb * C::kQBytes + r * C::kQPitch, src, a.D * 2, qfull(qb));
-        if (t0 == 0 && set.rows_at) {
-          // where the merge finds this row's partials: the unit's first, and how many
-          const int u0 = s_base + in_seq * nt;
-          set.rows_at[(int64_t)(q.q0 + j) * a.hq + h * a.G + g] =
-              make_int4(unit + (int)blockIdx.x, r, (u0 + nt - 1) / share - (int)blockIdx.x + 1, s);
-        }
-      }
-      ++seg;
-
-      for (int t = 0; t < nseg; ++t) {
-        const int k0 = (t0 + t) * kTile;
-        const int p0 = k0 >> ps;
-        if (p0 < pbase || p0 + pages_per_tile > pbase + 32) {
-          pbase = p0;
-          pcache = first_pages(s, pbase);
-        }
-        const int pg = __shfl_sync(0xffffffffu, pcache, min(p0 + min(i, pages_per_tile - 1) - pbase, 31));
-        const bool there = i < pages_per_tile && p0 + i <= last;
-        const bool good = there && pg >= 0 && pg < a.n_pages;
-        const uint32_t good_m = __ballot_sync(0xffffffffu, good);
-        if (there && !good) set_status(a.status, LILY_STATUS_BAD_PAGE);
-        ok = wait_warp(empty(stage), phase ^ 1, &abort_s, a.status);
-        if (!ok) break;
-        if (lane == 0) {
-          unsigned long long m = 0;
-          for (int p = 0; p < pages_per_tile; ++p)
-            if (good_m >> (p * 2 * halves) & 1u)
-              m |= (box_rows == 64 ? ~0ull : ((1ull << box_rows) - 1)) << (p * box_rows);
-          if (q.len - k0 < kTile) m &= (1ull << (q.len - k0)) - 1;
-          mask_s[stage] = m;
-          mbar_arrive_expect_tx(full(stage), __popc(good_m) * box_bytes);
-        }
-        __syncwarp();
-        if (good) {
-          const uint32_t dst = base + stage * C::kStageBytes + at_stage;
-          const int row = pages_per_tile > 1 ? 0 : k0 & ((1 << ps) - 1);
-          if (is_v) tma_load_4d(dst, &mv, hf * 64, row, h, pg, full(stage));
-          else tma_load_4d(dst, &mk, hf * 64, row, h, pg, full(stage));
-        }
-        __syncwarp();
-        used |= 1u << stage;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      at += nseg;
-      if (ok && at < end && at >= s_base + a.hkv * nb * nt) ok = find(at);
-    }
-    // no more units
-    if (ok) {
-      const int qb = seg % C::kQBufs;
-      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.status);
-      if (ok && lane == 0) {
-        desc[qb].part = -1;
-        mbar_arrive(qfull(qb));
-      }
-    }
-    if (!ok && lane == 0) {
-      // given up: this CTA's copies must have landed before its memory goes
-      int dead = 0;
-      if (seg > 0)
-        mbar_wait(qfull((seg - 1) % C::kQBufs), ((seg - 1) / C::kQBufs) & 1, &dead, a.status);
-      for (int j = 0; j < C::kStages; ++j)
-        if (used >> j & 1u) mbar_wait(full(j), j < stage ? phase : phase ^ 1, &dead, a.status);
-    }
-  } else {
-    // ------------------------------------------------------------- compute
-    const int wr = warp % WR, wk = warp / WR;
-    const int g8 = lane >> 2, c2 = (lane & 3) * 2;
-    constexpr int kNT = C::kKeys / 8;  // n-tiles of scores
-    const int key_w = wk * C::kKeys;   // this warp's first key in a tile
-    const float c = a.scale_log2;
-    int stage = 0, phase = 0;
-    bool ok = true;
-    for (int seg = 0;; ++seg) {
-      const int qb = seg % C::kQBufs;
-      if (ok) ok = wait_warp(qfull(qb), (seg / C::kQBufs) & 1, &abort_s, a.status);
-      // a warp whose wait gave up takes the others with it, so that none is
-      // left at a barrier
-      if (!ok && lane == 0) dead_s[seg & 1] = 1;
-      named_sync(1, 32 * kWarps);
-      if (*reinterpret_cast<volatile int*>(&dead_s[seg & 1])) break;
-      const Desc d = desc[qb];
-      if (d.part < 0) break;
-      const uint32_t qaddr = base + C::kQOff + qb * C::kQBytes +
-                             (wr * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * C::kQPitch +
-                             (lane >> 4) * 16;
-      uint32_t qf[C::kQRegs ? DP / 16 : 1][4];
-      if (C::kQRegs) {
-#pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) ldsm4(qaddr + ks * 32, qf[ks]);
-      }
-      const bool busy = wr * 16 < d.nrows;
-      // keys that each of the thread's two rows sees
-      const int ra = wr * 16 + g8, rb = ra + 8;
-      int lim_a = d.len, lim_b = d.len;
-      if (set.causal) {
-        lim_a = d.len - d.qn + 1 + (d.row0 + ra) / a.G;
-        lim_b = d.len - d.qn + 1 + (d.row0 + rb) / a.G;
-      }
-      const int lim_all = set.causal ? d.len - d.qn + 1 + d.row0 / a.G : d.len;  // least of the unit
-      // largest score, z = c * largest score (rounded once: every exponent and
-      // the final log use the same z), sum
-      float m_a = -INFINITY, m_b = -INFINITY, z_a = 0.f, z_b = 0.f, l_a = 0.f, l_b = 0.f;
-      float o[DP / 8][4];
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-      for (int t = 0; t < d.tiles; ++t) {
-        ok = wait_warp(full(stage), phase, &abort_s, a.status);
-        if (!ok) break;
-        if (busy) {
-          const uint32_t ks_base = base + stage * C::kStageBytes;
-          const uint32_t vs_base = ks_base + C::kTileBytes;
-          const int k0 = d.key0 + t * kTile;
-          const unsigned long long mask = mask_s[stage];
-          const bool masked = mask != ~0ull || k0 + kTile > lim_all;
-
-          float sc[kNT][4];
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-          const int krow = key_w + (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
-#pragma unroll
-          for (int ks = 0; ks < DP / 16; ++ks) {
-            uint32_t qt[4];
-            if (C::kQRegs) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) qt[e] = qf[C::kQRegs ? ks : 0][e];
-            } else {
-              ldsm4(qaddr + ks * 32, qt);
-            }
-#pragma unroll
-            for (int n = 0; n < kNT; n += 2) {
-              uint32_t b[4];
-              ldsm4(ks_base + (ks >> 2) * C::kHalfBytes + swz(krow + n * 8, (ks & 3) * 2 + kch), b);
-              mma16816<F16>(sc[n], qt, b[0], b[1]);
-              mma16816<F16>(sc[n + 1], qt, b[2], b[3]);
-            }
-          }
-          if (masked) {
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int k = key_w + n * 8 + c2 + e;
-                const bool there = mask >> k & 1ull;
-                if (!there || k0 + k >= lim_a) sc[n][e] = -INFINITY;
-                if (!there || k0 + k >= lim_b) sc[n][2 + e] = -INFINITY;
-              }
-          }
-          float x_a = m_a, x_b = m_b;
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            x_a = fmaxf(x_a, fmaxf(sc[n][0], sc[n][1]));
-            x_b = fmaxf(x_b, fmaxf(sc[n][2], sc[n][3]));
-          }
-          x_a = fmaxf(x_a, __shfl_xor_sync(0xffffffffu, x_a, 1));
-          x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, 1));
-          x_a = fmaxf(x_a, __shfl_xor_sync(0xffffffffu, x_a, 2));
-          x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, 2));
-          if (__any_sync(0xffffffffu, x_a != m_a || x_b != m_b)) {
-            // (a row that has seen nothing keeps z = 0 and has nothing to scale)
-            const float y_a = x_a == -INFINITY ? 0.f : __fmul_rn(x_a, c);
-            const float y_b = x_b == -INFINITY ? 0.f : __fmul_rn(x_b, c);
-            const float f_a = m_a == -INFINITY ? 0.f : ex2(z_a - y_a);
-            const float f_b = m_b == -INFINITY ? 0.f : ex2(z_b - y_b);
-            l_a *= f_a;
-            l_b *= f_b;
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) {
-              o[i][0] *= f_a;
-              o[i][1] *= f_a;
-              o[i][2] *= f_b;
-              o[i][3] *= f_b;
-            }
-            m_a = x_a;
-            m_b = x_b;
-            z_a = y_a;
-            z_b = y_b;
-          }
-          uint32_t pf[kNT / 2][4];
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            const float p0 = ex2(fmaf(sc[n][0], c, -z_a)), p1 = ex2(fmaf(sc[n][1], c, -z_a));
-            const float p2 = ex2(fmaf(sc[n][2], c, -z_b)), p3 = ex2(fmaf(sc[n][3], c, -z_b));
-            l_a += p0 + p1;
-            l_b += p2 + p3;
-            pf[n / 2][(n & 1) * 2] = pack16(p0, p1, F16);
-            pf[n / 2][(n & 1) * 2 + 1] = pack16(p2, p3, F16);
-          }
-          const int vrow = key_w + (lane & 7) + ((lane >> 3) & 1) * 8, vch = lane >> 4;
-          auto v_frag = [&](int kb, int i, uint32_t(&b)[4]) {
-            ldsm4_t(vs_base + (i >> 2) * C::kHalfBytes + swz(vrow + kb * 16, (i & 3) * 2 + vch), b);
-          };
-          // the thread's keys of block kb that are in m, as masks of V's two words
-          auto v_masks = [&](unsigned long long m, int kb, uint32_t& v0, uint32_t& v1) {
-            const uint32_t mb = (uint32_t)(m >> (key_w + kb * 16 + c2));
-            v0 = (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
-            v1 = (mb & 0x100u ? 0xffffu : 0u) | (mb & 0x200u ? 0xffff0000u : 0u);
-          };
-          // V of keys that a row does not see may hold anything, and 0 * NaN
-          // would reach its sum.  Keys that are not there are cut to zero for
-          // all rows.  Where a new token's V holds an infinity or NaN that
-          // some rows of the tile see and others do not, the tile's product
-          // is taken token by token with that token's keys alone.
-          bool split = false;
-          if (masked && set.causal && k0 + kTile > lim_all) {
-            const int seen = max(lim_all - k0, 0);  // keys every row sees
-            const unsigned long long some = mask & (seen < kTile ? ~0ull << seen : 0ull);
-            constexpr uint32_t kExp = F16 ? 0x7C00u : 0x7F80u;
-#pragma unroll
-            for (int kb = 0; kb < kNT / 2; ++kb) {
-              uint32_t v0, v1;
-              v_masks(some, kb, v0, v1);
-              if (!__any_sync(0xffffffffu, (v0 | v1) != 0)) continue;
-              for (int i = 0; i < DP / 16; ++i) {
-                uint32_t b[4];
-                v_frag(kb, i, b);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t w = b[e] & (e & 1 ? v1 : v0);
-                  split |= (w & kExp) == kExp || (w >> 16 & kExp) == kExp;
-                }
-              }
-            }
-            split = __any_sync(0xffffffffu, split);
-          }
-          if (!split) {
-#pragma unroll
-            for (int kb = 0; kb < kNT / 2; ++kb) {
-              uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;
-              if (masked) v_masks(mask, kb, v0, v1);
-#pragma unroll
-              for (int i = 0; i < DP / 16; ++i) {
-                uint32_t b[4];
-                v_frag(kb, i, b);
-                if (masked) {
-                  b[0] &= v0;
-                  b[1] &= v1;
-                  b[2] &= v0;
-                  b[3] &= v1;
-                }
-                mma16816<F16>(o[2 * i], pf[kb], b[0], b[1]);
-                mma16816<F16>(o[2 * i + 1], pf[kb], b[2], b[3]);
-              }
-            }
-          } else {
-            const int j1 = (d.row0 + wr * 16 + 15) / a.G;
-            for (int j = (d.row0 + wr * 16) / a.G; j <= j1; ++j) {
-              const int seen = d.len - d.qn + 1 + j - k0;
-              const unsigned long long m =
-                  mask & (seen <= 0 ? 0ull : seen < kTile ? (1ull << seen) - 1 : ~0ull);
-              const bool keep_a = (d.row0 + ra) / a.G == j, keep_b = (d.row0 + rb) / a.G == j;
-#pragma unroll
-              for (int i = 0; i < DP / 16; ++i) {
-                float x[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) x[n][e] = o[2 * i + n][e];
-#pragma unroll
-                for (int kb = 0; kb < kNT / 2; ++kb) {
-                  uint32_t b[4], v0, v1;
-                  v_masks(m, kb, v0, v1);
-                  v_frag(kb, i, b);
-                  mma16816<F16>(x[0], pf[kb], b[0] & v0, b[1] & v1);
-                  mma16816<F16>(x[1], pf[kb], b[2] & v0, b[3] & v1);
-                }
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                  if (keep_a) o[2 * i + n][0] = x[n][0];
-                  if (keep_a) o[2 * i + n][1] = x[n][1];
-                  if (keep_b) o[2 * i + n][2] = x[n][2];
-                  if (keep_b) o[2 * i + n][3] = x[n][3];
-                }
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(empty(stage));
-          // The first tile's products have used the fragments of Q: only now is
-          // the buffer free.  (Released right after the loads were issued, the
-          // next rows could land before these were read.)
-          if (C::kQRegs && t == 0) mbar_arrive(qempty(qb));
-        }
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      if (!C::kQRegs) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qempty(qb));
-      }
-
-      l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
-      l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
-      l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
-      l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-      float* part_o = set.part_o + (int64_t)d.part * C::kRows * a.D;
-      float* part_lse = set.part_lse + (int64_t)d.part * C::kRows;
-      auto lse2 = [&](float z, float l) { return l == 0.f ? -INFINITY : z + log2f(l); };
-      auto inverse = [](float l) { return l == 0.f ? 0.f : 1.f / l; };
-      if constexpr (C::kWK == 1) {
-        const float i_a = inverse(l_a), i_b = inverse(l_b);
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          const int col = i * 8 + c2;
-          if (col < a.D) {
-            if (ra < d.nrows)
-              *reinterpret_cast<float2*>(part_o + (int64_t)ra * a.D + col) =
-                  make_float2(o[i][0] * i_a, o[i][1] * i_a);
-            if (rb < d.nrows)
-              *reinterpret_cast<float2*>(part_o + (int64_t)rb * a.D + col) =
-                  make_float2(o[i][2] * i_b, o[i][3] * i_b);
-          }
-        }
-        if ((lane & 3) == 0) {
-          if (ra < d.nrows) part_lse[ra] = lse2(z_a, l_a);
-          if (rb < d.nrows) part_lse[rb] = lse2(z_b, l_b);
-        }
-      } else {
-        // the warps that split the keys put their rows together
-        float* red = reinterpret_cast<float*>(smem + C::kRedOff);
-        if ((lane & 3) == 0) {
-          red_z[warp][g8] = m_a == -INFINITY ? -INFINITY : z_a;
-          red_z[warp][g8 + 8] = m_b == -INFINITY ? -INFINITY : z_b;
-          red_l[warp][g8] = l_a;
-          red_l[warp][g8 + 8] = l_b;
-        }
-        named_sync(1, 32 * kWarps);
-        float M_a = -INFINITY, M_b = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < C::kWK; ++w) {
-          M_a = fmaxf(M_a, red_z[w * WR + wr][g8]);
-          M_b = fmaxf(M_b, red_z[w * WR + wr][g8 + 8]);
-        }
-        const float f_a = M_a == -INFINITY ? 0.f : ex2(red_z[warp][g8] - M_a);
-        const float f_b = M_b == -INFINITY ? 0.f : ex2(red_z[warp][g8 + 8] - M_b);
-        // this thread's share of the sums: four columns of one row
-        constexpr int kQuads = C::kRedCols / 4;
-        static_assert(C::kRows * kQuads == 32 * kWarps, "one quad of columns per thread");
-        const int orow = threadIdx.x / kQuads, oq = threadIdx.x % kQuads;
-        const int ob = orow >> 4, oi = orow & 15;  // row block, row in it
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < C::kWK; ++w) M = fmaxf(M, red_z[w * WR + ob][oi]);
-#pragma unroll
-        for (int w = 0; w < C::kWK; ++w)
-          if (M != -INFINITY) L += red_l[w * WR + ob][oi] * ex2(red_z[w * WR + ob][oi] - M);
-          else L += red_l[w * WR + ob][oi];  // 0, or NaN
-        const float inv = inverse(L);
-        if (oq == 0 && orow < d.nrows) part_lse[orow] = lse2(M == -INFINITY ? 0.f : M, L);
-#pragma unroll
-        for (int cb = 0; cb < DP / C::kRedCols; ++cb) {
-#pragma unroll
-          for (int n = 0; n < C::kRedCols / 8; ++n) {
-            const int i = cb * (C::kRedCols / 8) + n;
-            float* p = red + (warp * 16 + g8) * C::kRedPitch + n * 8 + c2;
-            *reinterpret_cast<float2*>(p) = make_float2(o[i][0] * f_a, o[i][1] * f_a);
-            *reinterpret_cast<float2*>(p + 8 * C::kRedPitch) =
-                make_float2(o[i][2] * f_b, o[i][3] * f_b);
-          }
-          named_sync(1, 32 * kWarps);
-          const int col = cb * C::kRedCols + oq * 4;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < C::kWK; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(
-                red + ((w * WR + ob) * 16 + oi) * C::kRedPitch + oq * 4);
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
-          }
-          if (orow < d.nrows && col < a.D)
-            *reinterpret_cast<float4*>(part_o + (int64_t)orow * a.D + col) =
-                make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-          named_sync(1, 32 * kWarps);
-        }
-      }
-    }
-  }
-  if (!first) pdl_wait();
-}
-
 // A query row (token, query head) per W warps, 8 / W rows per block: the
-// partials of the prefix and of the sequence's own keys, spread over the row's
-// warps, weighted by 2^(lse - largest lse) and added up.  rows_at may hold
-// anything for rows without own keys: an entry counts where its sequence has
-// the row's token and keys, for then this call has written it.
+// partials of the prefix and of the sequence's own keys, weighted by 2^(lse -
+// largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
+// finds the weight of one of them, then all lanes add up their outputs, up to
+// eight at a time.  What bounds it is the chain of loads (where a row's own
+// partials lie, its sequence, lse, output), so the prefix's lse are requested
+// with the first.  rows_at may hold anything for rows without own keys: an entry
+// counts where its sequence has the row's token and keys, for then this call
+// has written it.
 template <int W>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
-  __shared__ float acc_s[W > 1 ? 7 : 1][W > 1 ? 256 : 1];
+  __shared__ float acc_s[W > 1 ? 8 : 1][W > 1 ? 256 : 1];
+  __shared__ float2 ms_s[8];  // largest lse and sum of weights of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % W;  // of the row's warps
-  const int64_t row = (int64_t)blockIdx.x * (8 / W) + warp / W;
-  const bool live = row < (int64_t)a.T * a.hq;
+  const int rows = a.T * a.hq;  // (at most 2^30: 65536 tokens of 16384 heads)
+  const int row = blockIdx.x * (8 / W) + warp / W;
+  const bool live = row < rows;
+  const int t = row / a.hq, hq = row - t * a.hq;
+  // partials [p0, p0 + np) of the prefix at row pr
+  int p0 = 0, np = 0, pr = 0;
+  if (live && m.pre_tiles) {
+    const int h = hq / a.G;
+    const int r = t * a.G + hq - h * a.G;
+    const int u = h * m.pre_blocks + r / m.pre_rows;
+    const int c0 = u * m.pre_tiles / m.pre_share;
+    p0 = u + c0;
+    np = (((u + 1) * m.pre_tiles - 1) / m.pre_share - c0 + 1) * m.pre_streams;
+    pr = r % m.pre_rows;
+  }
+  auto pre_row = [&](int i) {  // row of partial i of the prefix
+    return m.pre_streams == 1
+               ? (int64_t)(p0 + i) * m.pre_slot_rows + pr
+               : (int64_t)(p0 + (i >> 1)) * m.pre_slot_rows + (i & 1) * 128 + pr;
+  };
   pdl_wait();
   pdl_trigger();
-
-  // partials [p0, p0 + np) of the prefix at row pr, [w0, w0 + nw) of the
-  // sequence at row wrow
-  int64_t p0 = 0, w0 = 0;
-  int np = 0, nw = 0, pr = 0, wrow = 0;
-  const int t = (int)(row / a.hq), hq = (int)(row - (int64_t)t * a.hq);
+  const int first = part + W * lane;
+  const float pre0 = first < np ? m.pre_lse[pre_row(first)] : -INFINITY;
+  // partials [w0, w0 + nw) of the sequence at row wrow
+  int w0 = 0, nw = 0, wrow = 0;
   if (live && m.own.rows_at) {
     const int4 at = m.own.rows_at[row];
     if (at.w >= 0 && at.w < m.own.n_seqs) {
@@ -733,74 +59,103 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
       }
     }
   }
-  if (live && m.pre_tiles) {
-    const int h = hq / a.G;
-    const int r = t * a.G + hq - h * a.G;
-    const int64_t u = (int64_t)h * m.pre_blocks + r / m.pre_rows;
-    const int64_t c0 = u * m.pre_tiles / m.pre_share;
-    const int64_t c1 = ((u + 1) * m.pre_tiles - 1) / m.pre_share;
-    p0 = u + c0;
-    np = ((int)(c1 - c0) + 1) * m.pre_streams;
-    pr = r % m.pre_rows;
-  }
   const int n = np + nw;
-  // row of partial i of the prefix
-  auto pre_row = [&](int i) {
-    return m.pre_streams == 1 ? (p0 + i) * m.pre_slot_rows + pr
-                              : (p0 + (i >> 1)) * m.pre_slot_rows + (i & 1) * 128 + pr;
-  };
-  auto lse_of = [&](int i) {
-    return i < np ? m.pre_lse[pre_row(i)] : m.own.part_lse[(w0 + i - np) * m.own.rows + wrow];
-  };
-  // the first 32 partials' weights stay in the lanes
-  const float lse0 = lane < n ? lse_of(lane) : -INFINITY;
-  float M = lse0;
-  for (int i = 32 + lane; i < n; i += 32) M = fmaxf(M, lse_of(i));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float Z = M == -INFINITY ? 0.f : M;
-  const float wt0 = lane < n ? exp2f(lse0 - Z) : 0.f;
-  float sum = wt0;
-  for (int i = 32 + lane; i < n; i += 32) sum += exp2f(lse_of(i) - Z);
-  sum = warp_sum(sum);
+  auto own_row = [&](int i) { return (int64_t)(w0 + i - np) * m.own.rows + wrow; };
 
+  float M = -INFINITY, sum = 0.f;
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-  for (int i = part; i < n; i += W) {
-    const float w = i < 32 ? __shfl_sync(0xffffffffu, wt0, i) : exp2f(lse_of(i) - Z);
-    if (w == 0.f) continue;  // (a partial that saw nothing has no output)
-    const float* o = i < np ? m.pre_o + pre_row(i) * a.D
-                            : m.own.part_o + ((w0 + i - np) * m.own.rows + wrow) * a.D;
+  for (int k0 = 0; part + W * k0 < n; k0 += 32) {
+    const int i = part + W * (k0 + lane);
+    float lse = k0 == 0 ? pre0 : i < np ? m.pre_lse[pre_row(i)] : -INFINITY;
+    if (i >= np && i < n) lse = m.own.part_lse[own_row(i)];
+    float x = lse;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (k * 128 + lane * 4 < a.D) {
-        const float4 v = *reinterpret_cast<const float4*>(o + k * 128 + lane * 4);
-        acc[k].x = fmaf(w, v.x, acc[k].x);
-        acc[k].y = fmaf(w, v.y, acc[k].y);
-        acc[k].z = fmaf(w, v.z, acc[k].z);
-        acc[k].w = fmaf(w, v.w, acc[k].w);
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    x = fmaxf(x, M);
+    const float z = x == -INFINITY ? 0.f : x;
+    const float wt = i < n ? exp2f(lse - z) : 0.f;
+    const float f = M == -INFINITY ? 0.f : exp2f(M - z);
+    M = x;
+    sum = sum * f + warp_sum(wt);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      acc[k].x *= f;
+      acc[k].y *= f;
+      acc[k].z *= f;
+      acc[k].w *= f;
+    }
+    const int cnt = min(32, (n - part - W * k0 + W - 1) / W);
+    auto add = [&](auto wide) {
+      constexpr int kWide = decltype(wide)::value;  // quads of columns per lane
+      constexpr int kAt = 8 / kWide;
+      for (int j0 = 0; j0 < cnt; j0 += kAt) {
+        float4 v[kAt][kWide];
+        float w[kAt];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+          w[j] = __shfl_sync(0xffffffffu, wt, min(j0 + j, 31));
+          if (j0 + j >= cnt) w[j] = 0.f;  // (a partial of weight 0 may have no output)
+          const int p = part + W * (k0 + j0 + j);
+          const float* o = p < np ? m.pre_o + pre_row(p) * a.D : m.own.part_o + own_row(p) * a.D;
+#pragma unroll
+          for (int k = 0; k < kWide; ++k) {
+            v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[j] != 0.f && k * 128 + lane * 4 < a.D)
+              v[j][k] = *reinterpret_cast<const float4*>(o + k * 128 + lane * 4);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAt; ++j)
+#pragma unroll
+          for (int k = 0; k < kWide; ++k) {
+            acc[k].x = fmaf(w[j], v[j][k].x, acc[k].x);
+            acc[k].y = fmaf(w[j], v[j][k].y, acc[k].y);
+            acc[k].z = fmaf(w[j], v[j][k].z, acc[k].z);
+            acc[k].w = fmaf(w[j], v[j][k].w, acc[k].w);
+          }
       }
+    };
+    if (a.D <= 128) add(std::integral_constant<int, 1>());
+    else add(std::integral_constant<int, 2>());
   }
   if (W > 1) {
-    // row r's warp `part` (from 1 on) leaves its sums for its first warp
-    const int at = warp / W * (W - 1) + part - 1;
+    // the row's first warp puts its warps' sums together
+    if (lane == 0) ms_s[warp] = make_float2(M, sum);
     if (part > 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<float4*>(&acc_s[W > 1 ? at : 0][k * 128 + lane * 4]) = acc[k];
+        *reinterpret_cast<float4*>(&acc_s[W > 1 ? warp : 0][k * 128 + lane * 4]) = acc[k];
     }
     __syncthreads();
     if (part > 0) return;
-    for (int w = 0; w < W - 1; ++w)
+    float top = M;
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, ms_s[W > 1 ? warp + w : 0].x);
+    const float z = top == -INFINITY ? 0.f : top;
+    const float f0 = M == -INFINITY ? (sum != sum ? 1.f : 0.f) : exp2f(M - z);
+    sum *= f0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      acc[k].x *= f0;
+      acc[k].y *= f0;
+      acc[k].z *= f0;
+      acc[k].w *= f0;
+    }
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float2 o = ms_s[W > 1 ? warp + w : 0];
+      const float f = o.x == -INFINITY ? (o.y != o.y ? 1.f : 0.f) : exp2f(o.x - z);
+      sum += o.y * f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(
-            &acc_s[W > 1 ? warp / W * (W - 1) + w : 0][k * 128 + lane * 4]);
-        acc[k].x += v.x;
-        acc[k].y += v.y;
-        acc[k].z += v.z;
-        acc[k].w += v.w;
+        const float4 v = *reinterpret_cast<const float4*>(&acc_s[W > 1 ? warp + w : 0][k * 128 + lane * 4]);
+        acc[k].x = fmaf(f, v.x, acc[k].x);
+        acc[k].y = fmaf(f, v.y, acc[k].y);
+        acc[k].z = fmaf(f, v.z, acc[k].z);
+        acc[k].w = fmaf(f, v.w, acc[k].w);
       }
+    }
+    M = top;
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -814,23 +169,6 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
   if (m.lse && lane == 0) m.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int DP, int WR, bool F16>
-cudaError_t launch_keys_as(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
-                           const CUtensorMap& mv, bool first, cudaStream_t s) {
-  auto kern = attn_keys_kernel<DP, WR, F16>;
-  const cudaError_t e = ensure_smem_attr((const void*)kern, Cfg<DP, WR>::kBytes);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(set.grid), dim3(kThreads), Cfg<DP, WR>::kBytes, s, a, set, mk, mv,
-                    first);
-}
-template <int DP, bool F16>
-cudaError_t launch_keys_dp(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
-                           const CUtensorMap& mv, bool first, cudaStream_t s) {
-  return set.rows == 16   ? launch_keys_as<DP, 1, F16>(a, set, mk, mv, first, s)
-         : set.rows == 32 ? launch_keys_as<DP, 2, F16>(a, set, mk, mv, first, s)
-                          : launch_keys_as<DP, 4, F16>(a, set, mk, mv, first, s);
-}
-
 }  // namespace
 
 int attn_grid(int D) {
@@ -842,37 +180,32 @@ int attn_grid(int D) {
   return g < kAttnMaxGrid ? g : kAttnMaxGrid;
 }
 
-cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
-                             const CUtensorMap& mv, bool first, cudaStream_t s) {
+cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& pa, const AttnSet& pb,
+                             const CUtensorMap& mk, const CUtensorMap& mv, bool first,
+                             cudaStream_t s) {
   prof_begin(K_ATTN_KEYS, s);
-  const int dp = padded_dim(a.D);
-  cudaError_t e;
-  if (a.f16)
-    e = dp == 64    ? launch_keys_dp<64, true>(a, set, mk, mv, first, s)
-        : dp == 128 ? launch_keys_dp<128, true>(a, set, mk, mv, first, s)
-                    : launch_keys_dp<256, true>(a, set, mk, mv, first, s);
-  else
-    e = dp == 64    ? launch_keys_dp<64, false>(a, set, mk, mv, first, s)
-        : dp == 128 ? launch_keys_dp<128, false>(a, set, mk, mv, first, s)
-                    : launch_keys_dp<256, false>(a, set, mk, mv, first, s);
+  const cudaError_t e = a.f16 ? launch_attn_keys_f16(a, pa, pb, mk, mv, first, s)
+                              : launch_attn_keys_bf16(a, pa, pb, mk, mv, first, s);
   prof_end(K_ATTN_KEYS, s);
   return e;
 }
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s) {
   prof_begin(K_ATTN_MERGE, s);
-  // warps for a row's partials: the prefix's are known here, a sequence's own
-  // lengths only on the device
+  // Warps for a row: one per eight partials (the prefix's are known here, a
+  // sequence's own lengths only on the device), more where rows are too few to
+  // give every SM two blocks.
   int n = 1;
   if (m.pre_tiles) n += (m.pre_tiles / m.pre_share + 2) * m.pre_streams;
   const int64_t rows = (int64_t)a.T * a.hq;
-  auto launch = [&](auto kern, int w) {
-    const int per = 8 / w;
-    return launch_pdl(kern, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a, m);
-  };
-  const cudaError_t e = n <= 8    ? launch(attn_merge_kernel<1>, 1)
-                        : n <= 32 ? launch(attn_merge_kernel<4>, 4)
-                                  : launch(attn_merge_kernel<8>, 8);
+  int w = 1;
+  while (w < 8 && (n > 8 * w || (n >= 4 * w && rows * w < 8 * 2 * 152))) w *= 2;
+  const dim3 grid((unsigned)((rows * w + 7) / 8));
+  auto launch = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, s, a, m); };
+  const cudaError_t e = w == 1   ? launch(attn_merge_kernel<1>)
+                        : w == 2 ? launch(attn_merge_kernel<2>)
+                        : w == 4 ? launch(attn_merge_kernel<4>)
+                                 : launch(attn_merge_kernel<8>);
   prof_end(K_ATTN_MERGE, s);
   return e;
 }

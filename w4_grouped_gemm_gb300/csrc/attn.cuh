@@ -110,15 +110,56 @@ struct MergeArgs {
 };
 
 constexpr int kAttnTile = 64;      // keys of a tile
+// Head dimension that the kernels are built for: D rounded up.
+__host__ __device__ constexpr int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 constexpr int kAttnMaxGrid = 512;  // CTAs of a key kernel, at most (sizes the workspace)
 
 // CTAs of the key kernel on the current device for a head of D elements.
 int attn_grid(int D);
-// The partials of one set; first: the call's first launch (attn.cu).
-cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
-                             const CUtensorMap& mv, bool first, cudaStream_t s);
+// The partials of the prefix (pa) and the own pages (pb; not fewer rows in pa),
+// or of one set (pb.grid 0); first: the call's first launch (attn.cu).
+cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& pa, const AttnSet& pb,
+                             const CUtensorMap& mk, const CUtensorMap& mv, bool first,
+                             cudaStream_t s);
+cudaError_t launch_attn_keys_bf16(const AttnArgs& a, const AttnSet& pa, const AttnSet& pb,
+                                  const CUtensorMap& mk, const CUtensorMap& mv, bool first,
+                                  cudaStream_t s);
+cudaError_t launch_attn_keys_f16(const AttnArgs& a, const AttnSet& pa, const AttnSet& pb,
+                                 const CUtensorMap& mk, const CUtensorMap& mv, bool first,
+                                 cudaStream_t s);
 // Their merge into out and lse.
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s);
+
+// ---------------------------------------------------------------- sequences
+// A sequence's query tokens and own keys, held inside the call's bounds.
+struct SeqInfo {
+  int q0, qn, len;
+  bool bad;
+};
+__device__ __forceinline__ SeqInfo seq_info(const AttnSet& s, int T, int i) {
+  SeqInfo r;
+  r.bad = false;
+  int q1;
+  if (s.q_start) {
+    r.q0 = s.q_start[i];
+    q1 = s.q_start[i + 1];
+  } else {
+    r.q0 = i * s.max_q_len;
+    q1 = r.q0 + s.max_q_len;
+  }
+  if (r.q0 < 0 || r.q0 > T || q1 < r.q0 || q1 > T || q1 - r.q0 > s.max_q_len) {
+    r.bad = true;
+    r.q0 = min(max(r.q0, 0), T);
+    q1 = min(max(q1, r.q0), min(T, r.q0 + s.max_q_len));
+  }
+  r.qn = q1 - r.q0;
+  r.len = s.lens ? s.lens[i] : s.max_len;
+  if (r.len < 0 || r.len > s.max_len) {
+    r.bad = true;
+    r.len = min(max(r.len, 0), s.max_len);
+  }
+  return r;
+}
 
 // ---------------------------------------------------------------- copies, waits, 2^x
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int c0, int c1,

@@ -347,7 +347,6 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     m.pre_share = (int)((p.pre_total + used - 1) / used);
     m.pre_o = part_o;
     m.pre_lse = part_lse;
-    cudaError_t e;
     if (p.tc) {
       TcArgs& t = p.ptc;
       t.pages = prefix_pages;
@@ -362,7 +361,8 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
       m.pre_slot_rows = attn_tc_rows(a.D);
       m.pre_streams = !t.paired && a.D <= 128 ? 2 : 1;
       if (!maps(kTcKeys, attn_tc_v_keys(a.D))) return LILY_ERR_CUDA;
-      e = launch_attn_prefix_tc(a, t, mk, mv, s);
+      if (launch_attn_prefix_tc(a, t, mk, mv, s) != cudaSuccess) return LILY_ERR_CUDA;
+      first = false;
     } else {
       AttnSet& t = p.pre;
       t.table = prefix_pages;
@@ -373,11 +373,7 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
       m.pre_blocks = t.row_blocks;
       m.pre_rows = m.pre_slot_rows = t.rows;
       m.pre_streams = 1;
-      if (!maps(kAttnTile, kAttnTile)) return LILY_ERR_CUDA;
-      e = launch_attn_keys(a, t, mk, mv, first, s);
     }
-    if (e != cudaSuccess) return LILY_ERR_CUDA;
-    first = false;
   }
   if (d.max_seq_len) {
     AttnSet& o = p.own;
@@ -390,8 +386,13 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     o.rows_at = reinterpret_cast<int4*>(base + p.rows_at);
     o.grid = (int)(p.own_most < grid ? p.own_most : grid);
     m.own = o;
+  }
+  // the sets that mma.sync takes, in one launch
+  if (p.pre.grid + p.own.grid) {
     if (!maps(kAttnTile, kAttnTile)) return LILY_ERR_CUDA;
-    if (launch_attn_keys(a, o, mk, mv, first, s) != cudaSuccess) return LILY_ERR_CUDA;
+    const bool pre = p.pre.grid > 0;
+    if (launch_attn_keys(a, pre ? p.pre : p.own, pre ? p.own : AttnSet{}, mk, mv, first, s) != cudaSuccess)
+      return LILY_ERR_CUDA;
   }
   return rc_of(launch_attn_merge(a, m, s));
 }

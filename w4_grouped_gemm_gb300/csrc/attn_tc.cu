@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       const int row0 = run.unit % p.row_blocks * p.block_rows + (paired ? g * 128 : 0);
       const int nrows = min(128, rows_all - row0);  // may be 0 or less
       // rows of Q, 16 bytes at a time, swizzled; zeros past the rows and past D
-      // (a warp brings its own 32 rows, eight per thread, whose loads of a block
+      // (a warp brings its own 32 rows, eight per thread, whose loads of two blocks
       // are in flight together)
       {
         const int e = lane & 7;
@@ -502,20 +502,26 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           const int rr = row0 + r, j = rr / a.G, gg = rr - j * a.G;
           at[i] = r < nrows ? (int64_t)j * a.q_tok + (int64_t)(h * a.G + gg) * a.q_head : -1;
         }
-        for (int k = 0; k < blocks; ++k) {
-          const int col = k * 64 + e * 8;
-          uint4 v[8];
+        for (int k = 0; k < blocks; k += 2) {
+          uint4 v[2][8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            v[i] = at[i] >= 0 && col < a.D
-                       ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i] + col)
-                       : make_uint4(0, 0, 0, 0);
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = quad * 32 + i * 4 + (lane >> 3);
-            *reinterpret_cast<uint4*>(smem + g * C::kQTile + k * 128 * 128 + r * 128 +
-                                      ((e ^ (r & 7)) << 4)) = v[i];
-          }
+            for (int i = 0; i < 8; ++i) {
+              const int col = (k + m) * 64 + e * 8;
+              v[m][i] = make_uint4(0, 0, 0, 0);
+              if (at[i] >= 0 && col < a.D)
+                v[m][i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at[i] + col);
+            }
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            if (k + m < blocks)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = quad * 32 + i * 4 + (lane >> 3);
+                *reinterpret_cast<uint4*>(smem + g * C::kQTile + (k + m) * 128 * 128 + r * 128 +
+                                          ((e ^ (r & 7)) << 4)) = v[m][i];
+              }
         }
       }
       fence_proxy_async_smem();
