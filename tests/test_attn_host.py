@@ -26,7 +26,7 @@ def L():
 
 def _with(s, **kw):
     c = type(s)()
-    ctypes.memmove(ctypes.byref(c), ctypes.byref(s), ctypes.sizeof(s))
+    ctypes.memmove(c._at, s._at, ctypes.sizeof(s))
     for k, v in kw.items():
         setattr(c, k, v)
     return c
@@ -45,7 +45,7 @@ def test_header_functions_exported(L):
 
 
 def _norm(L, dims, x=P, res=P, w=P, res_out=P, out=P, scales=None):
-    return L.lily_attn_add_rmsnorm(ctypes.byref(dims) if dims else None, x, res, w, res_out, out,
+    return L.lily_attn_add_rmsnorm(dims._at if dims else None, x, res, w, res_out, out,
                                    scales, None)
 
 
@@ -87,8 +87,8 @@ BAD_CACHES = [(dict(k=None), ARG), (dict(v=None), ARG), (dict(n_pages=0), ARG),
 
 
 def _rope(L, dims, cache=CACHE, q=P, k=P, v=P, pos=P, slots=P, freq=P, qo=P, ws=P, n=256):
-    return L.lily_attn_rope_append(ctypes.byref(dims) if dims else None,
-                                   ctypes.byref(cache) if cache else None, q, k, v, pos, slots,
+    return L.lily_attn_rope_append(dims._at if dims else None,
+                                   cache._at if cache else None, q, k, v, pos, slots,
                                    freq, qo, ws, n, None)
 
 
@@ -123,20 +123,20 @@ ATTN = _attn.AttnDims(8, 16, 8, 1, 1000, 640, 10, 0.1, 2048, 128, 2048, 128)
 
 
 def _attn_call(L, dims, cache=CACHE, q=P, pre=P, qs=P, lens=P, table=P, out=P, lse=P, ws=P, n=BIG):
-    return L.lily_attn_shared_prefix(ctypes.byref(dims) if dims else None,
-                                     ctypes.byref(cache) if cache else None, q, pre, qs, lens,
+    return L.lily_attn_shared_prefix(dims._at if dims else None,
+                                     cache._at if cache else None, q, pre, qs, lens,
                                      table, out, lse, ws, n, None)
 
 
 def test_attention_refusals(L):
-    need = L.lily_attn_workspace_bytes(ctypes.byref(ATTN), ctypes.byref(CACHE))
+    need = L.lily_attn_workspace_bytes(ATTN._at, CACHE._at)
     assert need > 256
     assert _attn_call(L, None) == ARG and _attn_call(L, ATTN, cache=None) == ARG
-    assert L.lily_attn_workspace_bytes(None, ctypes.byref(CACHE)) == 0
+    assert L.lily_attn_workspace_bytes(None, CACHE._at) == 0
     for bad, code in BAD_CACHES:
         c = _with(CACHE, **bad)
         assert _attn_call(L, ATTN, cache=c) == code, bad
-        assert L.lily_attn_workspace_bytes(ctypes.byref(ATTN), ctypes.byref(c)) == 0
+        assert L.lily_attn_workspace_bytes(ATTN._at, c._at) == 0
     for name in ("q", "pre", "lens", "table", "out", "ws"):
         assert _attn_call(L, ATTN, **{name: None}) == ARG, name
     for name in ("q", "pre", "qs", "lens", "table", "out", "lse", "ws"):

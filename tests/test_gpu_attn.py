@@ -302,6 +302,14 @@ def test_bad_lengths_are_clamped(oracle_lib):
     b.check(out, lse)
 
 
+def test_bad_lengths_among_many_sequences(oracle_lib):
+    """The same where the sequences are summed by groups, and the bad one's group has no keys."""
+    n = 70
+    b = Batch(own=[5] * 32 + [0] * (n - 32), prefix=20, seed=19)
+    out, lse = b.run(lens=[5] * 32 + [0] * (n - 33) + [-1], status=lily.LILY_STATUS_BAD_LEN)
+    b.check(out, lse)
+
+
 def test_non_finite_values_of_unseen_tokens(oracle_lib):
     """A later token's K and V hold NaN and infinities: the rows before it do not see them, its own
     row and those after do."""

@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import LILY_ERR_INVALID_ARG, LilyError, _check, _ptr, _stream
+from ._lib import LILY_ERR_INVALID_ARG, LilyError, _check, _raw_stream, _stream
 
 LILY_DTYPE_F16 = 2
 LILY_DTYPE_E4M3 = 3
@@ -27,7 +27,15 @@ _DTYPES = {torch.bfloat16: _lib.LILY_DTYPE_BF16, torch.float32: _lib.LILY_DTYPE_
            torch.float16: LILY_DTYPE_F16, torch.float8_e4m3fn: LILY_DTYPE_E4M3}
 
 
-class NormDims(ctypes.Structure):
+class _Struct(ctypes.Structure):
+    """A struct passed by address; the address is looked up once."""
+
+    def __init__(self, *values):
+        super().__init__(*values)
+        self._at = ctypes.addressof(self)
+
+
+class NormDims(_Struct):
     _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "w_dtype",
                                                "out_dtype", "group")]
                 + [("eps", ctypes.c_float)]
@@ -35,21 +43,21 @@ class NormDims(ctypes.Structure):
                                                  "out_stride")])
 
 
-class Cache(ctypes.Structure):
+class Cache(_Struct):
     _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
                 + [(n, ctypes.c_int32) for n in ("dtype", "n_pages", "page_size", "n_kv_heads",
                                                  "head_dim")]
                 + [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")])
 
 
-class RopeDims(ctypes.Structure):
+class RopeDims(_Struct):
     _fields_ = ([(n, ctypes.c_int32) for n in ("T", "n_q_heads", "rotary_dim", "style")]
                 + [(n, ctypes.c_int64) for n in (
                     "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
                     "v_token_stride", "v_head_stride", "qo_token_stride", "qo_head_stride")])
 
 
-class AttnDims(ctypes.Structure):
+class AttnDims(_Struct):
     _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_seqs", "max_q_len",
                                                "prefix_len", "max_seq_len", "table_stride")]
                 + [("scale", ctypes.c_float)]
@@ -65,13 +73,12 @@ def _L():
     if _attn is None:
         L = _lib.lib()
         P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-        ref = ctypes.POINTER
+        # dims and cache structs go by the address that their objects keep (_at)
         sig = {
-            "lily_attn_add_rmsnorm": (I, [ref(NormDims), P, P, P, P, P, P, P]),
-            "lily_attn_rope_append": (I, [ref(RopeDims), ref(Cache), P, P, P, P, P, P, P, P, SZ, P]),
-            "lily_attn_workspace_bytes": (SZ, [ref(AttnDims), ref(Cache)]),
-            "lily_attn_shared_prefix": (I, [ref(AttnDims), ref(Cache), P, P, P, P, P, P, P, P, SZ,
-                                            P]),
+            "lily_attn_add_rmsnorm": (I, [P, P, P, P, P, P, P, P]),
+            "lily_attn_rope_append": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "lily_attn_workspace_bytes": (SZ, [P, P]),
+            "lily_attn_shared_prefix": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -85,15 +92,29 @@ def _refuse(what):
     raise LilyError(LILY_ERR_INVALID_ARG, what)
 
 
-def _gpu(what, *tensors):
+def _ptrs(what, tensors):
+    """Addresses of GPU tensors (or addresses as they are; None stays)."""
+    out = []
     for t in tensors:
-        if t is not None and not isinstance(t, int) and not t.is_cuda:
+        if t is None or t.__class__ is int:
+            out.append(t)
+        elif t.is_cuda:
+            out.append(t.data_ptr())
+        else:
             _refuse(f"{what}: a tensor is not on the GPU")
+    return out
 
 
 def _typed(what, name, t, dtype):
-    if t is not None and not isinstance(t, int) and (t.dtype is not dtype or not t.is_contiguous()):
+    if t is not None and t.__class__ is not int and (t.dtype is not dtype or not t.is_contiguous()):
         _refuse(f"{what}: {name} must be a contiguous {dtype} tensor")
+
+
+def _on(stream, tensor):
+    """A stream's handle; by default the current stream of the tensor's device."""
+    if stream is None and _raw_stream is not None and tensor.__class__ is not int:
+        return _raw_stream(tensor.get_device())
+    return _stream(stream)
 
 
 def _code(dtype) -> int:
@@ -113,7 +134,7 @@ class PagedCache:
         if (k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype
                 or k.stride(3) != 1):
             _refuse("cache: k and v must be 4-D, alike in shape, strides and type, last stride 1")
-        _gpu("cache", k, v)
+        _ptrs("cache", (k, v))
         token, head = (1, 2) if layout == "nhd" else (2, 1)
         self.k, self.v, self.layout = k, v, layout
 
@@ -135,10 +156,10 @@ def make_norm_dims(T, d, x_dtype, res_dtype, w_dtype, out_dtype, group=0, eps=1e
 def lily_attn_add_rmsnorm(dims: NormDims, x, residual, weight, residual_out, out, scales=None,
                           stream=None):
     """residual_out = x + residual; out = its RMSNorm (see the header)."""
-    _gpu("lily_attn_add_rmsnorm", x, residual, weight, residual_out, out, scales)
-    _check(_L().lily_attn_add_rmsnorm(ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(weight),
-                                      _ptr(residual_out), _ptr(out), _ptr(scales),
-                                      _stream(stream)), "lily_attn_add_rmsnorm")
+    p = _ptrs("lily_attn_add_rmsnorm", (x, residual, weight, residual_out, out, scales))
+    rc = _L().lily_attn_add_rmsnorm(dims._at, *p, _on(stream, x))
+    if rc:
+        _check(rc, "lily_attn_add_rmsnorm")
 
 
 def _strides(t, what):
@@ -166,13 +187,13 @@ def lily_attn_rope_append(dims: RopeDims, cache: PagedCache, q, k, v, positions,
                           q_out, ws, stream=None):
     """Rotate q into q_out and k, append k and v at `slots` (see the header)."""
     what = "lily_attn_rope_append"
-    _gpu(what, q, k, v, positions, slots, inv_freq, q_out, ws)
+    p = _ptrs(what, (q, k, v, positions, slots, inv_freq, q_out, ws))
     _typed(what, "positions", positions, torch.int32)
     _typed(what, "slots", slots, torch.int64)
     _typed(what, "inv_freq", inv_freq, torch.float64)
-    _check(_L().lily_attn_rope_append(ctypes.byref(dims), ctypes.byref(cache.c), _ptr(q), _ptr(k),
-                                      _ptr(v), _ptr(positions), _ptr(slots), _ptr(inv_freq),
-                                      _ptr(q_out), _ptr(ws), ws.numel(), _stream(stream)), what)
+    rc = _L().lily_attn_rope_append(dims._at, cache.c._at, *p, ws.numel(), _on(stream, ws))
+    if rc:
+        _check(rc, what)
 
 
 def make_attn_dims(q, out, n_seqs, max_q_len, prefix_len, max_seq_len, table_stride,
@@ -183,19 +204,18 @@ def make_attn_dims(q, out, n_seqs, max_q_len, prefix_len, max_seq_len, table_str
 
 
 def lily_attn_workspace_bytes(dims: AttnDims, cache: PagedCache) -> int:
-    return int(_L().lily_attn_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache.c)))
+    return int(_L().lily_attn_workspace_bytes(dims._at, cache.c._at))
 
 
 def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, q_start, seq_lens,
                             block_table, out, lse, ws, stream=None):
     """Attention over the shared prefix and each sequence's own pages (see the header)."""
     what = "lily_attn_shared_prefix"
-    _gpu(what, q, prefix_pages, q_start, seq_lens, block_table, out, lse, ws)
+    p = _ptrs(what, (q, prefix_pages, q_start, seq_lens, block_table, out, lse, ws))
     _typed(what, "prefix_pages", prefix_pages, torch.int32)
     _typed(what, "q_start", q_start, torch.int32)
     _typed(what, "seq_lens", seq_lens, torch.int32)
     _typed(what, "block_table", block_table, torch.int32)
-    _check(_L().lily_attn_shared_prefix(ctypes.byref(dims), ctypes.byref(cache.c), _ptr(q),
-                                        _ptr(prefix_pages), _ptr(q_start), _ptr(seq_lens),
-                                        _ptr(block_table), _ptr(out), _ptr(lse), _ptr(ws),
-                                        ws.numel(), _stream(stream)), what)
+    rc = _L().lily_attn_shared_prefix(dims._at, cache.c._at, *p, ws.numel(), _on(stream, q))
+    if rc:
+        _check(rc, what)

@@ -1,5 +1,6 @@
 // attn.cu -- the merge of attention's partial outputs, and the launches of
 // lily_attn_shared_prefix's kernels (attn_keys.cuh, attn_tc.cu).
+#include <atomic>
 #include <type_traits>
 
 #include "attn.cuh"
@@ -11,13 +12,14 @@ namespace {
 // partials of the prefix and of the sequence's own keys, weighted by 2^(lse -
 // largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
 // finds the weight of one of them, then all lanes add up their outputs, up to
-// eight at a time.  What bounds it is the chain of loads (where a row's own
+// four at a time (eight took 122 registers, and the rows then waited for a place
+// on the SMs: 15 us for 8192 rows of one partial).  What bounds it is the chain of loads (where a row's own
 // partials lie, its sequence, lse, output), so the prefix's lse are requested
 // with the first.  rows_at may hold anything for rows without own keys: an entry
 // counts where its sequence has the row's token and keys, for then this call
 // has written it.
 template <int W>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
+__global__ void __launch_bounds__(256, 4) attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
   __shared__ float acc_s[W > 1 ? 8 : 1][W > 1 ? 256 : 1];
   __shared__ float2 ms_s[8];  // largest lse and sum of weights of a warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
     const int cnt = min(32, (n - part - W * k0 + W - 1) / W);
     auto add = [&](auto wide) {
       constexpr int kWide = decltype(wide)::value;  // quads of columns per lane
-      constexpr int kAt = 8 / kWide;
+      constexpr int kAt = 4 / kWide;
       for (int j0 = 0; j0 < cnt; j0 += kAt) {
         float4 v[kAt][kWide];
         float w[kAt];
@@ -172,10 +174,14 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a, const
 }  // namespace
 
 int attn_grid(int D) {
+  static std::atomic<int> known[64];  // SMs of a device, once asked; 0: not yet
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
   const int g = sms * (padded_dim(D) <= 128 ? 2 : 1);
   return g < kAttnMaxGrid ? g : kAttnMaxGrid;
 }
@@ -192,14 +198,14 @@ cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& pa, const AttnSet
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s) {
   prof_begin(K_ATTN_MERGE, s);
-  // Warps for a row: one per eight partials (the prefix's are known here, a
+  // Warps for a row: one per four partials (the prefix's are known here, a
   // sequence's own lengths only on the device), more where rows are too few to
   // give every SM two blocks.
   int n = 1;
   if (m.pre_tiles) n += (m.pre_tiles / m.pre_share + 2) * m.pre_streams;
   const int64_t rows = (int64_t)a.T * a.hq;
   int w = 1;
-  while (w < 8 && (n > 8 * w || (n >= 4 * w && rows * w < 8 * 2 * 152))) w *= 2;
+  while (w < 8 && (n > 4 * w || (n >= 2 * w && rows * w < 8 * 2 * 152))) w *= 2;
   const dim3 grid((unsigned)((rows * w + 7) / 8));
   auto launch = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, s, a, m); };
   const cudaError_t e = w == 1   ? launch(attn_merge_kernel<1>)

@@ -59,7 +59,7 @@ struct AttnSet {
   const int32_t* lens;     // NULL: every sequence has max_len keys
   const int32_t* table;
   int n_seqs, max_q_len, max_len, table_stride;
-  int rows, row_blocks;    // 16, 32 or 64; ceil(max_q_len * G / rows)
+  int rows, row_blocks;    // 8, 16, 32 or 64; ceil(max_q_len * G / rows)
   int causal;              // query j of q sees keys 0 .. len - q + j
   int min_share;           // tiles a CTA takes, at least
   int grid;                // CTAs; at most one per tile

@@ -65,8 +65,8 @@ int check_attn_dims(const lily_attn_dims* d, const lily_attn_cache* c) {
   return LILY_OK;
 }
 
-// Rows per unit: 16, 32 or 64, the least that holds `rows` (64 at most).
-int unit_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows per unit: 8, 16, 32 or 64, the least that holds `rows` (64 at most).
+int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 // Query rows per KV head from which the prefix goes to the tensor-core kernel:
 // above one mma.sync row block.
@@ -83,13 +83,14 @@ struct Plan {
   size_t pre_o, pre_lse, own_o, own_lse, rows_at, bytes;
 };
 
-void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G) {
+void set_shape(AttnSet& s, int n_seqs, int max_q_len, int max_len, int G, int least_rows = 8) {
   s = AttnSet{};
   s.n_seqs = n_seqs;
   s.max_q_len = max_q_len;
   s.max_len = max_len;
   const int64_t rows = (int64_t)max_q_len * G;
   s.rows = unit_rows(rows);
+  if (s.rows < least_rows) s.rows = least_rows;
   s.row_blocks = (int)((rows + s.rows - 1) / s.rows);
   s.min_share = 1;
 }
@@ -130,7 +131,13 @@ bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   }
   // (no sequence has more tokens than the call)
   const int max_q_len = d.max_q_len < d.n_tokens ? d.max_q_len : d.n_tokens;
-  set_shape(p.own, d.n_seqs, max_q_len, d.max_seq_len, G);
+  // (pairs of row counts that share a launch: the smaller is 8, or the larger, or
+  // 16 beside 64)
+  int least = 8;
+  const int own_rows = unit_rows((int64_t)max_q_len * G);
+  if (p.pre.rows == 32 && own_rows == 16) least = 32;
+  if (p.pre.rows == 64 && own_rows == 32) least = 64;
+  set_shape(p.own, d.n_seqs, max_q_len, d.max_seq_len, G, least);
   p.own.causal = max_q_len > 1;
   const int64_t units = (int64_t)d.n_seqs * c.n_kv_heads * p.own.row_blocks;
   if (units > INT_MAX / 2) return false;
@@ -143,6 +150,25 @@ bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   }
   p.bytes = off;
   return true;
+}
+
+// CTAs for the prefix's A tiles and the own pages' B tiles (at most) in one
+// launch on a GPU that holds `cap`.  Either both sets take all it holds, one
+// after the other, or they share it; a CTA costs about three tiles of time
+// besides its own.  B is a bound only, so the prefix never gets less than half.
+void share_grid(int cap, int64_t A, int64_t B, int& ga, int& gb) {
+  ga = (int)(A < cap ? A : cap);
+  gb = (int)(B < cap ? B : cap);
+  if (ga + gb <= cap) return;
+  auto per = [](int64_t n, int g) { return (n + g - 1) / g; };
+  int sa = cap - gb > cap / 2 ? cap - gb : cap / 2;
+  if (A < sa) sa = (int)A;
+  const int sb = cap - sa;
+  const int64_t both = per(A, sa) > per(B, sb) ? per(A, sa) : per(B, sb);
+  if (both + 3 <= per(A, ga) + per(B, gb) + 6) {
+    ga = sa;
+    gb = sb;
+  }
 }
 
 // The cache as a 4-D tensor [page][head][token][D]; boxes of 64 dimensions
@@ -336,13 +362,15 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
   m.out_tok = d.out_token_stride;
   m.out_head = d.out_head_stride;
 
+  int pre_grid, own_grid;
+  share_grid(grid, p.tc ? 0 : p.pre_total, p.own_most, pre_grid, own_grid);
   bool first = true;
   if (d.prefix_len) {
     float* part_o = reinterpret_cast<float*>(base + p.pre_o);
     float* part_lse = reinterpret_cast<float*>(base + p.pre_lse);
     // one tensor-core CTA per SM
     const int64_t sms = grid / (cache->head_dim <= 128 ? 2 : 1);
-    const int64_t most = !p.tc ? grid : sms < kTcMaxGrid ? sms : kTcMaxGrid;
+    const int64_t most = !p.tc ? pre_grid : sms < kTcMaxGrid ? sms : kTcMaxGrid;
     const int used = (int)(p.pre_total < most ? p.pre_total : most);
     m.pre_share = (int)((p.pre_total + used - 1) / used);
     m.pre_o = part_o;
@@ -384,7 +412,7 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     o.part_o = reinterpret_cast<float*>(base + p.own_o);
     o.part_lse = reinterpret_cast<float*>(base + p.own_lse);
     o.rows_at = reinterpret_cast<int4*>(base + p.rows_at);
-    o.grid = (int)(p.own_most < grid ? p.own_most : grid);
+    o.grid = own_grid;
     m.own = o;
   }
   // the sets that mma.sync takes, in one launch

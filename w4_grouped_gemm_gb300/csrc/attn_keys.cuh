@@ -33,10 +33,11 @@ constexpr int kThreads = 32 * (kWarps + 1);     // and the producer
 constexpr int kTile = kAttnTile;
 
 // DP: head dimension rounded up to 64, 128 or 256 (the rest reads as zero);
-// WR: blocks of 16 rows.
-template <int DP, int WR>
+// ROWS: query rows of a unit, 8, 16, 32 or 64 (8 fill both halves of an mma's 16).
+template <int DP, int ROWS>
 struct Cfg {
-  static constexpr int kRows = 16 * WR;
+  static constexpr int kRows = ROWS;
+  static constexpr int WR = ROWS <= 16 ? 1 : ROWS / 16;  // blocks of 16 rows
   static constexpr int kWK = kWarps / WR;        // warps that split a tile's keys
   static constexpr int kKeys = kTile / kWK;      // keys of a warp
   static constexpr int kOcc = DP <= 128 ? 2 : 1;
@@ -44,16 +45,18 @@ struct Cfg {
   static constexpr int kHalfBytes = kTile * 128;             // 64 keys x 64 dimensions
   static constexpr int kTileBytes = kHalfBytes * (DP / 64);  // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // Q: up to 128 dimensions live in registers during a unit, so one buffer
-  // is free again at once; 256 stay in shared memory (rows padded by 16 bytes)
+  // Q: up to 128 dimensions live in registers during a unit; 256 stay in shared
+  // memory (rows padded by 16 bytes).  Several units' rows are brought ahead
+  // where units are short: with one buffer the next unit's K and V waited for
+  // its Q, and a unit of one key took 7 us.
   static constexpr bool kQRegs = DP <= 128;
   static constexpr int kQPitch = kQRegs ? DP * 2 : DP * 2 + 16;
-  static constexpr int kQBufs = kQRegs || WR > 1 ? 1 : 2;
+  static constexpr int kQBufs = ROWS == 8 ? (DP == 256 ? 3 : 4) : ROWS == 16 ? 2 : 1;
   static constexpr int kQBytes = kRows * kQPitch;
   // columns of O that the warps of a row block exchange at a time
-  static constexpr int kRedCols = WR == 1 ? 32 : 16;
-  static constexpr int kRedPitch = kRedCols + 4;
-  static constexpr int kRedBytes = kWK > 1 ? kWarps * 16 * kRedPitch * 4 : 0;
+  static constexpr int kRedRows = ROWS < 16 ? ROWS : 16;
+  static constexpr int kRedCols = ROWS == 8 ? 64 : ROWS == 16 ? 32 : 16;
+  static constexpr int kRedBytes = kWK > 1 ? kWarps * kRedRows * kRedCols * 4 : 0;
   static constexpr int kQOff = kStages * kStageBytes;
   static constexpr int kRedOff = kQOff + kQBufs * kQBytes;
   static constexpr int kBytes = kRedOff + kRedBytes;
@@ -103,19 +106,32 @@ __device__ __forceinline__ int blocks_of(const AttnSet& s, int G, int qn) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
+// Shared memory of any of the variants beside stages, Q and the exchange.
+struct Fixed {
+  static constexpr int kMaxStages = 6, kMaxQBufs = 4;
+  uint64_t bars[2 * kMaxStages + 2 * kMaxQBufs];
+  Desc desc[kMaxQBufs];
+  unsigned long long mask[kMaxStages];  // valid keys of a stage
+  float red_z[kWarps][16], red_l[kWarps][16];
+  int abort;
+  int dead[2];  // compute warps agree at each unit whether to go on
+};
+
 // Partials of one set: CTA `cta` of its `set.grid`.
-template <int DP, int WR, bool F16>
+template <int DP, int ROWS, bool F16>
 __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set, const CUtensorMap& mk,
                                           const CUtensorMap& mv, bool first, int cta,
-                                          uint8_t* smem) {
-  using C = Cfg<DP, WR>;
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 * C::kQBufs];
-  __shared__ Desc desc[C::kQBufs];
-  __shared__ unsigned long long mask_s[C::kStages];  // valid keys of a stage
-  __shared__ int total_s[kWarps + 1];
-  __shared__ float red_z[kWarps][16], red_l[kWarps][16];
-  __shared__ int abort_s;
-  __shared__ int dead_s[2];  // compute warps agree at each unit whether to go on
+                                          uint8_t* smem, Fixed& fx) {
+  using C = Cfg<DP, ROWS>;
+  constexpr int WR = C::WR;
+  static_assert(C::kStages <= Fixed::kMaxStages && C::kQBufs <= Fixed::kMaxQBufs, "shared memory");
+  auto& bars = fx.bars;
+  auto& desc = fx.desc;
+  auto& mask_s = fx.mask;
+  auto& red_z = fx.red_z;
+  auto& red_l = fx.red_l;
+  auto& abort_s = fx.abort;
+  auto& dead_s = fx.dead;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
@@ -151,27 +167,28 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       if (i % (C::kTileBytes / 16) >= halves * (C::kHalfBytes / 16))
         reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-
+  __syncthreads();
   if (first) pdl_wait();
   pdl_trigger();
 
-  // the set's tiles (31 bits: checked on the host), and this CTA's run of them
+  // The set's tiles (31 bits: checked on the host).  Up to 32 sequences: the
+  // producer has them in its lanes.  More: 32 at a time by all warps, which
+  // leave the groups' sums in the first stage.
   auto cost_of = [&](const SeqInfo& q) { return a.hkv * blocks_of(set, a.G, q.qn) * tiles_of(q.len); };
-  int sum = 0;
-  for (int i = threadIdx.x; i < set.n_seqs; i += kThreads) {
-    const SeqInfo q = seq_info(set, a.T, i);
-    if (q.bad && cta == 0) set_status(a.status, LILY_STATUS_BAD_LEN);
-    sum += cost_of(q);
+  const int groups = (set.n_seqs + 31) / 32;
+  int* sums = reinterpret_cast<int*>(smem);
+  if (groups > 1) {
+    for (int g = warp; g < groups; g += kWarps + 1) {
+      const int i = g * 32 + lane;
+      SeqInfo q = {};
+      if (i < set.n_seqs) q = seq_info(set, a.T, i);
+      if (q.bad && cta == 0) set_status(a.status, LILY_STATUS_BAD_LEN);
+      const int c = __reduce_add_sync(0xffffffffu, cost_of(q));
+      if (lane == 0) sums[g] = c;
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) total_s[warp] = sum;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w <= kWarps; ++w) total += total_s[w];
-  const int share = max((total + set.grid - 1) / set.grid, set.min_share);
-  const int begin = (int)min((int64_t)share * cta, (int64_t)total);
-  const int end = min(begin + share, total);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
@@ -191,7 +208,6 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
     const int hf = rest - (is_v ? halves : 0);
     const uint32_t at_stage = (is_v ? C::kTileBytes : 0) + hf * C::kHalfBytes + i * box_bytes;
 
-    int at = begin;
     int s0 = -1, s = 0;       // sequences s0 .. s0 + 31 lie in the lanes; current one
     int s_base = 0;           // first tile of sequence s
     SeqInfo mine = {};        // of sequence s0 + lane
@@ -200,6 +216,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       s0 = first_seq;
       mine = SeqInfo{};
       if (s0 + lane < set.n_seqs) mine = seq_info(set, a.T, s0 + lane);
+      if (mine.bad && groups == 1 && cta == 0) set_status(a.status, LILY_STATUS_BAD_LEN);
       my_cost = s0 + lane < set.n_seqs ? cost_of(mine) : 0;
       int inc = my_cost;
 #pragma unroll
@@ -209,6 +226,40 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       }
       my_base = base_tile + inc - my_cost;
     };
+    // total tiles, and the group that holds this CTA's first
+    int total = 0, group = 0, group_base = 0;
+    if (groups == 1) {
+      load32(0, 0);
+      total = __reduce_add_sync(0xffffffffu, my_cost);
+    } else {
+      for (int g = lane; g < groups; g += 32) total += sums[g];
+      total = __reduce_add_sync(0xffffffffu, total);
+    }
+    const int share = max((total + set.grid - 1) / set.grid, set.min_share);  // tiles per CTA
+    const int begin = (int)min((int64_t)share * cta, (int64_t)total);
+    const int end = min(begin + share, total);
+    int at = begin;
+    if (groups > 1) {
+      for (int g0 = 0; g0 < groups; g0 += 32) {
+        const int c = g0 + lane < groups ? sums[g0 + lane] : 0;
+        int inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, group_base + inc > begin);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          group = g0 + l;
+          group_base += __shfl_sync(0xffffffffu, inc - c, l);
+          break;
+        }
+        group_base += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      __syncwarp();
+      fence_proxy_async_smem();
+    }
     // the sequence that holds tile t, from the current group on; false past the last
     auto find = [&](int t) {
       for (;;) {
@@ -230,7 +281,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
     };
     int pseq = -1, pbase = 0, pcache = 0, next_cache = 0;
     if (at < end) {
-      load32(0, 0);
+      if (groups > 1) load32(group * 32, group_base);
       ok = find(at);
     }
     while (ok && at < end) {
@@ -367,7 +418,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       const Desc d = desc[qb];
       if (d.part < 0) break;
       const uint32_t qaddr = base + C::kQOff + qb * C::kQBytes +
-                             (wr * 16 + (lane & 7) + ((lane >> 3) & 1) * 8) * C::kQPitch +
+                             (wr * 16 + (lane & 7) + (ROWS > 8 ? ((lane >> 3) & 1) * 8 : 0)) * C::kQPitch +
                              (lane >> 4) * 16;
       uint32_t qf[C::kQRegs ? DP / 16 : 1][4];
       if (C::kQRegs) {
@@ -625,6 +676,10 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
         const float f_b = M_b == -INFINITY ? 0.f : ex2(red_z[warp][g8 + 8] - M_b);
         // this thread's share of the sums: four columns of one row
         constexpr int kQuads = C::kRedCols / 4;
+        // (word of a row's column: pieces of 8 columns swizzled by the row)
+        auto word = [&](int w, int r, int col) {
+          return (w * C::kRedRows + r) * C::kRedCols + (col ^ ((r & (C::kRedCols / 8 - 1)) << 3));
+        };
         static_assert(C::kRows * kQuads == 32 * kWarps, "one quad of columns per thread");
         const int orow = threadIdx.x / kQuads, oq = threadIdx.x % kQuads;
         const int ob = orow >> 4, oi = orow & 15;  // row block, row in it
@@ -642,18 +697,18 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
 #pragma unroll
           for (int n = 0; n < C::kRedCols / 8; ++n) {
             const int i = cb * (C::kRedCols / 8) + n;
-            float* p = red + (warp * 16 + g8) * C::kRedPitch + n * 8 + c2;
-            *reinterpret_cast<float2*>(p) = make_float2(o[i][0] * f_a, o[i][1] * f_a);
-            *reinterpret_cast<float2*>(p + 8 * C::kRedPitch) =
-                make_float2(o[i][2] * f_b, o[i][3] * f_b);
+            *reinterpret_cast<float2*>(red + word(warp, g8, n * 8 + c2)) =
+                make_float2(o[i][0] * f_a, o[i][1] * f_a);
+            if (ROWS > 8)
+              *reinterpret_cast<float2*>(red + word(warp, g8 + 8, n * 8 + c2)) =
+                  make_float2(o[i][2] * f_b, o[i][3] * f_b);
           }
           named_sync(1, 32 * kWarps);
           const int col = cb * C::kRedCols + oq * 4;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < C::kWK; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(
-                red + ((w * WR + ob) * 16 + oi) * C::kRedPitch + oq * 4);
+            const float4 u = *reinterpret_cast<const float4*>(red + word(w * WR + ob, oi, oq * 4));
             v.x += u.x;
             v.y += u.y;
             v.z += u.z;
@@ -674,20 +729,21 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
 // predecessor and waits for it; else it follows the prefix's launch on the
 // tensor cores, which has waited, and only ends after it (so that the merge,
 // which waits for this launch, sees both).
-template <int DP, int WRA, int WRB, bool F16>
-__global__ void __launch_bounds__(kThreads, Cfg<DP, WRA>::kOcc)
+template <int DP, int RA, int RB, bool F16>
+__global__ void __launch_bounds__(kThreads, Cfg<DP, RA>::kOcc)
     attn_keys_kernel(const AttnArgs a, const AttnSet pa, const AttnSet pb,
                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                      bool first) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Fixed fx;
   const int cta = (int)blockIdx.x;
-  if (WRA == WRB) {
+  if (RA == RB) {
     const bool second = cta >= pa.grid;
-    keys_body<DP, WRA, F16>(a, second ? pb : pa, mk, mv, first, second ? cta - pa.grid : cta, smem);
+    keys_body<DP, RA, F16>(a, second ? pb : pa, mk, mv, first, second ? cta - pa.grid : cta, smem, fx);
   } else if (cta < pa.grid) {
-    keys_body<DP, WRA, F16>(a, pa, mk, mv, first, cta, smem);
+    keys_body<DP, RA, F16>(a, pa, mk, mv, first, cta, smem, fx);
   } else {
-    keys_body<DP, WRB, F16>(a, pb, mk, mv, first, cta - pa.grid, smem);
+    keys_body<DP, RB, F16>(a, pb, mk, mv, first, cta - pa.grid, smem, fx);
   }
   if (!first) pdl_wait();
 }
@@ -699,11 +755,11 @@ struct KeysLaunch {
   bool first;
   cudaStream_t s;
 };
-template <int DP, int WRA, int WRB, bool F16>
+template <int DP, int RA, int RB, bool F16>
 cudaError_t launch_keys_as(const KeysLaunch& l) {
-  auto kern = attn_keys_kernel<DP, WRA, WRB, F16>;
+  auto kern = attn_keys_kernel<DP, RA, RB, F16>;
   constexpr int kBytes =
-      Cfg<DP, WRA>::kBytes > Cfg<DP, WRB>::kBytes ? Cfg<DP, WRA>::kBytes : Cfg<DP, WRB>::kBytes;
+      Cfg<DP, RA>::kBytes > Cfg<DP, RB>::kBytes ? Cfg<DP, RA>::kBytes : Cfg<DP, RB>::kBytes;
   const cudaError_t e = ensure_smem_attr((const void*)kern, kBytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(l.pa.grid + l.pb.grid), dim3(kThreads), kBytes, l.s, l.a, l.pa, l.pb,
@@ -711,12 +767,14 @@ cudaError_t launch_keys_as(const KeysLaunch& l) {
 }
 template <int DP, bool F16>
 cudaError_t launch_keys_dp(const KeysLaunch& l) {
+  // (the pairs of rows that attn_api.cu plans)
   const int ra = l.pa.rows, rb = l.pb.grid ? l.pb.rows : ra;
-  if (ra == 16) return launch_keys_as<DP, 1, 1, F16>(l);
-  if (ra == 32) return rb == 16 ? launch_keys_as<DP, 2, 1, F16>(l) : launch_keys_as<DP, 2, 2, F16>(l);
-  return rb == 16   ? launch_keys_as<DP, 4, 1, F16>(l)
-         : rb == 32 ? launch_keys_as<DP, 4, 2, F16>(l)
-                    : launch_keys_as<DP, 4, 4, F16>(l);
+  if (ra == 8) return launch_keys_as<DP, 8, 8, F16>(l);
+  if (ra == 16) return rb == 8 ? launch_keys_as<DP, 16, 8, F16>(l) : launch_keys_as<DP, 16, 16, F16>(l);
+  if (ra == 32) return rb == 8 ? launch_keys_as<DP, 32, 8, F16>(l) : launch_keys_as<DP, 32, 32, F16>(l);
+  return rb == 8    ? launch_keys_as<DP, 64, 8, F16>(l)
+         : rb == 16 ? launch_keys_as<DP, 64, 16, F16>(l)
+                    : launch_keys_as<DP, 64, 64, F16>(l);
 }
 
 template <bool F16>
