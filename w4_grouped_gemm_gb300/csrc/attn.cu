@@ -8,7 +8,8 @@
 namespace lily {
 namespace {
 
-// A query row (token, query head) per W warps, 8 / W rows per block: the
+// A query row (token, query head) per W warps, 8 / W rows per block (W 32: one
+// row in a block of 32 warps): the
 // partials of the prefix and of the sequence's own keys, weighted by 2^(lse -
 // largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
 // finds the weight of one of them, then all lanes add up their outputs, up to
@@ -19,13 +20,16 @@ namespace {
 // counts where its sequence has the row's token and keys, for then this call
 // has written it.
 template <int W>
-__global__ void __launch_bounds__(256, 4) attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
-  __shared__ float acc_s[W > 1 ? 8 : 1][W > 1 ? 256 : 1];
-  __shared__ float2 ms_s[8];  // largest lse and sum of weights of a warp
+__global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 1 : 4)
+    attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
+  constexpr int kWarps = W > 8 ? W : 8, kRows = kWarps / W;  // of a block
+  __shared__ __align__(16) float acc_s[W > 1 ? kWarps : 1][W > 1 ? 256 : 4];
+  __shared__ float2 ms_s[kWarps];  // largest lse and sum of weights of a warp
+  __shared__ float f_s[kWarps], inv_s[kRows];  // a warp's factor, a row's last one
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = warp % W;  // of the row's warps
   const int rows = a.T * a.hq;  // (at most 2^30: 65536 tokens of 16384 heads)
-  const int row = blockIdx.x * (8 / W) + warp / W;
+  const int row = blockIdx.x * kRows + warp / W;
   const bool live = row < rows;
   const int t = row / a.hq, hq = row - t * a.hq;
   // partials [p0, p0 + np) of the prefix at row pr
@@ -121,43 +125,52 @@ __global__ void __launch_bounds__(256, 4) attn_merge_kernel(const AttnArgs a, co
     else add(std::integral_constant<int, 2>());
   }
   if (W > 1) {
-    // the row's first warp puts its warps' sums together
+    // the warps' sums through shared memory, added up by all threads
     if (lane == 0) ms_s[warp] = make_float2(M, sum);
-    if (part > 0) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<float4*>(&acc_s[W > 1 ? warp : 0][k * 128 + lane * 4]) = acc[k];
-    }
+    for (int k = 0; k < 2; ++k)
+      *reinterpret_cast<float4*>(&acc_s[W > 1 ? warp : 0][W > 1 ? k * 128 + lane * 4 : 0]) = acc[k];
     __syncthreads();
-    if (part > 0) return;
-    float top = M;
-#pragma unroll
-    for (int w = 1; w < W; ++w) top = fmaxf(top, ms_s[W > 1 ? warp + w : 0].x);
-    const float z = top == -INFINITY ? 0.f : top;
-    const float f0 = M == -INFINITY ? (sum != sum ? 1.f : 0.f) : exp2f(M - z);
-    sum *= f0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      acc[k].x *= f0;
-      acc[k].y *= f0;
-      acc[k].z *= f0;
-      acc[k].w *= f0;
-    }
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-      const float2 o = ms_s[W > 1 ? warp + w : 0];
-      const float f = o.x == -INFINITY ? (o.y != o.y ? 1.f : 0.f) : exp2f(o.x - z);
-      sum += o.y * f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(&acc_s[W > 1 ? warp + w : 0][k * 128 + lane * 4]);
-        acc[k].x = fmaf(f, v.x, acc[k].x);
-        acc[k].y = fmaf(f, v.y, acc[k].y);
-        acc[k].z = fmaf(f, v.z, acc[k].z);
-        acc[k].w = fmaf(f, v.w, acc[k].w);
+    if (threadIdx.x < kWarps) {
+      const int r = threadIdx.x / W;
+      float top = -INFINITY, total = 0.f;
+      for (int w = 0; w < W; ++w) top = fmaxf(top, ms_s[r * W + w].x);
+      const float z = top == -INFINITY ? 0.f : top;
+      auto factor = [&](float2 o) {  // (NaN sums stay)
+        return o.x == -INFINITY ? (o.y != o.y ? 1.f : 0.f) : exp2f(o.x - z);
+      };
+      f_s[threadIdx.x] = factor(ms_s[threadIdx.x]);
+      if (threadIdx.x % W == 0) {
+        for (int w = 0; w < W; ++w) total += ms_s[r * W + w].y * factor(ms_s[r * W + w]);
+        inv_s[r] = total == 0.f ? 0.f : 1.f / total;
+        const int64_t to = (int64_t)blockIdx.x * kRows + r;
+        if (m.lse && to < rows)
+          m.lse[to] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
       }
     }
-    M = top;
+    __syncthreads();
+    const int quads = a.D >> 2;
+    for (int i = threadIdx.x; i < kRows * quads; i += 32 * kWarps) {
+      const int r = i / quads, c = 4 * (i - r * quads);
+      const int to = blockIdx.x * kRows + r;
+      if (to >= rows) break;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int w = 0; w < W; ++w) {
+        const float f = f_s[r * W + w];
+        const float4 x = *reinterpret_cast<const float4*>(&acc_s[W > 1 ? r * W + w : 0][W > 1 ? c : 0]);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+      }
+      const float inv = inv_s[r];
+      const int tt = to / a.hq, hh = to - tt * a.hq;
+      uint16_t* out = static_cast<uint16_t*>(m.out) + (int64_t)tt * m.out_tok + (int64_t)hh * m.out_head;
+      *reinterpret_cast<uint2*>(out + c) = make_uint2(pack16(v.x * inv, v.y * inv, a.f16),
+                                                      pack16(v.z * inv, v.w * inv, a.f16));
+    }
+    return;
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -206,12 +219,17 @@ cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_
   const int64_t rows = (int64_t)a.T * a.hq;
   int w = 1;
   while (w < 8 && (n > 4 * w || (n >= 2 * w && rows * w < 8 * 2 * 152))) w *= 2;
-  const dim3 grid((unsigned)((rows * w + 7) / 8));
-  auto launch = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, s, a, m); };
+  if (n > 32) w = 32;
+  const int per = w > 8 ? 1 : 8 / w;
+  const dim3 grid((unsigned)((rows + per - 1) / per));
+  auto launch = [&](auto kern) {
+    return launch_pdl(kern, grid, dim3(w > 8 ? 32 * w : 256), 0, s, a, m);
+  };
   const cudaError_t e = w == 1   ? launch(attn_merge_kernel<1>)
                         : w == 2 ? launch(attn_merge_kernel<2>)
                         : w == 4 ? launch(attn_merge_kernel<4>)
-                                 : launch(attn_merge_kernel<8>);
+                        : w == 8 ? launch(attn_merge_kernel<8>)
+                                 : launch(attn_merge_kernel<32>);
   prof_end(K_ATTN_MERGE, s);
   return e;
 }
