@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
                           const __grid_constant__ CUtensorMap mv) {
   using C = Tc<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 12];
+  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 10];
   __shared__ __align__(16) uint32_t mask_s[kMasks][4];
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   const uint32_t bar1 = bar0 + 8 * 2 * C::kSlots;
   auto q_full = [&](int g) { return bar1 + 8 * g; };        // rows of Q in place
   auto s_full = [&](int b) { return bar1 + 8 * (2 + b); };  // scores in buffer b
-  auto p_full = [&](int b) { return bar1 + 8 * (4 + b); };  // probabilities in buffer b
+  // probabilities in buffer b (four softmax warps), and the turn to use them
+  auto p_full = [&](int b) { return bar1 + 8 * (4 + b); };
   auto o_full = [&](int g) { return bar1 + 8 * (6 + g); };  // product added to stream g's output
-  auto turn = [&](int g) { return bar1 + 8 * (8 + g); };    // stream g may issue its MMAs
-  const uint32_t land = bar1 + 8 * 10, drain = bar1 + 8 * 11;
+  const uint32_t land = bar1 + 8 * 8, drain = bar1 + 8 * 9;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -168,9 +168,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(q_full(i), 4);
         mbar_init(s_full(i), 1);
-        mbar_init(p_full(i), 4);
+        mbar_init(p_full(i), 5);
         mbar_init(o_full(i), 1);
-        mbar_init(turn(i), 1);
       }
       mbar_init(land, 1);
       mbar_init(drain, C::kGroups);
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   const bool paired = p.paired != 0;
 
   if (warp < kCtrlWarps) {
-    if (C::kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (C::kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 || warp == 2) {
       // --------------------------------------------------------- producers
       // One warp for K, one for V: a tile's boxes go out from one lane each
@@ -346,14 +345,12 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       // Two streams issue by turns, P V of a tile and Q K of the next together:
       // their MMAs and softmaxes so stay out of step, each under the other's.
       // (Left alone they fall into step and the pipe idles during both
-      // softmaxes.)  The turn is passed on before the last MMAs go out, so that
-      // the other warp wakes up in time.
+      // softmaxes.)  The turn is the fifth arrival on p_full, from the warp that
+      // issued before, sent before its last MMAs; a first product, or a stream
+      // alone, gives it to itself.  (On a barrier of its own it cost 250 cycles
+      // more of each product's way.)
       bool turns = false;
-      uint32_t turn_par = g == 0 ? 1 : 0;  // (stream 0 begins)
-      auto my_turn = [&]() {
-        if (turns) ok = ok && wait_warp(turn(g), turn_par, &abort_s, a.status);
-        turn_par ^= turns;
-      };
+      int next_buf = -1;  // buffer whose product follows, -1: none
       // (the next three: by one elected thread)
       // the n slots from x on are free once this stream's MMAs so far are
       // done (and the other stream's too, where it shares them)
@@ -373,7 +370,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
               x.skip(1);
               k = desc_k(slots + x.slot * C::kSlot);
             }
-            if (turns && c == blocks - 1) mbar_arrive(turn(g ^ 1));
+            if (next_buf >= 0 && c == blocks - 1) mbar_arrive(p_full(next_buf));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               mma_ss(d, q + c * (128 * 128 / 16) + 2 * i,
@@ -423,9 +420,9 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         for (int t = 0; t < min(ahead, n); ++t) {
           if (every || t == g) {
             take(cur, k_slots);
-            my_turn();
             if (!ok) break;
             tc_fence_after();
+            next_buf = -1;
             if (elect_one()) qk(paired ? g : t, cur);
             __syncwarp();
           }
@@ -437,34 +434,32 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           nk.skip(C::kVSlots);
           if (every || (t & 1) == g) {
             const int buf = paired ? g : t & 1;
+            // the first product of all, and every one of a stream alone
+            if ((!turns || (t == 0 && g == 0)) && lane == 0) mbar_arrive(p_full(buf));
+            next_buf = !turns ? -1 : paired ? (g == 0 ? 1 : more ? 0 : -1) : t + 1 < n ? buf ^ 1 : -1;
             take(cur, C::kVSlots);
             if (more && C::kGroups == 2) take(nk, k_slots);
             ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.status);
             p_par ^= 1u << buf;
-            my_turn();
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
               pv(buf, cur, paired || C::kGroups == 1 ? t == 0 : t < 2);
               if (more && C::kGroups == 2) qk(buf, nk);
-              if (!more && turns) mbar_arrive(turn(g ^ 1));
+              else if (next_buf >= 0) mbar_arrive(p_full(next_buf));
             }
             __syncwarp();
             if (more && C::kGroups == 1) {  // (the ring holds less than two tiles)
               take(nk, k_slots);
               if (!ok) break;
               tc_fence_after();
+              next_buf = -1;
               if (elect_one()) qk(buf, nk);
               __syncwarp();
             }
           }
           cur = nk;
           if (more) cur.skip(k_slots);
-        }
-        // with an odd number of turns the other stream would begin next
-        if (turns && g == 1 && !paired && (n & 1)) {
-          my_turn();
-          if (lane == 0) mbar_arrive(turn(0));
         }
       }
       if (!ok) {
@@ -478,7 +473,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    if (C::kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if (C::kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int g = (warp - kCtrlWarps) >> 2;          // stream
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // tensor memory lane field
