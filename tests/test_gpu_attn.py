@@ -223,6 +223,21 @@ def test_wide_rows_peaked_and_bad_pages(oracle_lib, D):
         b.check(out, lse)
 
 
+# CTAs that go on from one unit to the next: from a unit with one row block to one with two, from few
+# tiles to many, with both streams, one, or one that alternates
+@pytest.mark.parametrize("D,hq,hkv,seqs,prefix", [(96, 28, 4, 44, 5000), (128, 15, 3, 100, 4000),
+                                                  (64, 6, 3, 50, 9000), (128, 4, 2, 30, 30000),
+                                                  (256, 8, 4, 45, 5000), (192, 1, 1, 360, 9000),
+                                                  (256, 8, 1, 40, 20000)])
+def test_units_in_a_row(oracle_lib, D, hq, hkv, seqs, prefix):
+    b = Batch(hq=hq, hkv=hkv, D=D, own=[1 + i % 3 for i in range(seqs)], prefix=prefix, page=128,
+              dtype=H, seed=seqs)
+    out, lse = b.run()
+    again, lse2 = b.run(repeat=8)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    b.check(out, lse, skip=[s for s in range(seqs) if s % 6])    # every sixth, to keep the CPU's part short
+
+
 def test_batch_that_fills_the_gpu(oracle_lib):
     """More units than CTAs, cut at other places than their ends."""
     Batch(hq=2, hkv=2, D=64, own=[(97 * i) % 700 + 1 for i in range(350)], seed=8).go()

@@ -156,7 +156,12 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   auto s_full = [&](int b) { return bar1 + 8 * (2 + b); };  // scores in buffer b
   // probabilities in buffer b (four softmax warps), and the turn to use them
   auto p_full = [&](int b) { return bar1 + 8 * (4 + b); };
-  auto o_full = [&](int g) { return bar1 + 8 * (6 + g); };  // product added to stream g's output
+  // product added to the output: one barrier per stream; where one stream
+  // alternates between two buffers, one per buffer.  (A wait names a phase by
+  // its parity alone, so it must never be two phases off.  A stream with a
+  // buffer to itself has its scores after the product before; an alternating
+  // one hands P over while the product before may still run.)
+  auto o_full = [&](int i) { return bar1 + 8 * (6 + i); };
   const uint32_t land = bar1 + 8 * 8, drain = bar1 + 8 * 9;
 
   if (warp == 0) {
@@ -271,7 +276,10 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         Pos mine = cur;
         mine.skip(min(c, n_slots - 1));
         const uint32_t slot = slots + mine.slot * C::kSlot;
-        if (!(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.status))) return;
+        // (slot by slot: a warp's slots are up to a whole ring apart, and a wait
+        // for a slot holds only once the filling before is known to be done)
+        if (C::kVSlots > 1) ok = wait_warp(empty(cur.slot), cur.par ^ 1, &abort_s, a.status);
+        if (!ok || !(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.status))) return;
         const bool cut = is_v && !whole;
         const uint32_t bar = cut ? land : full(mine.slot);
         if (cut ? lane == 0 : active && in_slot == 0)
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
                              1u << 16;  // B is N-major
       Pos cur = {0, 0};    // slot of the current step
       uint32_t p_par = 0;  // parity of buffer b's P: bit b
-      int q_par = 0, frees = 1;
+      int q_par = 0;
       bool ok = true;
       auto take = [&](Pos x, int n) {  // the n slots from x on have arrived
         for (int j = 0; j < n && ok; ++j, x.skip(1))
@@ -352,11 +360,10 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       bool turns = false;
       int next_buf = -1;  // buffer whose product follows, -1: none
       // (the next three: by one elected thread)
-      // the n slots from x on are free once this stream's MMAs so far are
-      // done (and the other stream's too, where it shares them)
+      // the n slots from x on are free once this stream's MMAs so far are done
+      // and the other stream's warp has let them go too
       auto release = [&](Pos x, int n) {
-        for (int j = 0; j < n; ++j, x.skip(1))
-          for (int k = 0; k < frees; ++k) mma_commit(empty(x.slot));
+        for (int j = 0; j < n; ++j, x.skip(1)) mma_commit(empty(x.slot));
       };
       // S[buf] = Q K^T with K in the slots from x on; passes the turn
       auto qk = [&](int buf, Pos x) {
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           }
           mma_ts(d, pt + k * 8, v + k % (C::kVKeys / 16) * (16 * 128 / 16), id_pv, k != 0 || !fresh);
         }
-        mma_commit(o_full(g));
+        mma_commit(o_full(C::kGroups == 2 ? g : buf));
         release(v_pos, C::kVSlots);
       };
       while (ok && run.next()) {
@@ -400,63 +407,78 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         const int n = run.n;
         const bool shared = paired && left > 128;
         turns = C::kGroups == 2 && (paired ? shared : n > 1);
-        frees = C::kGroups == 2 && !shared ? 2 : 1;
         if (!(ok = wait_warp(q_full(g), q_par, &abort_s, a.status))) break;
         q_par ^= 1;
-        if (g == 1 && !turns) {
-          // nothing for this stream: its softmax warps wait for this, so that
-          // they do not run ahead
-          if (lane == 0) mbar_arrive(s_full(1));
-          for (int t = 0; t < n; ++t) {
-            cur.skip(k_slots);
-            cur.skip(C::kVSlots);
-          }
-          continue;
-        }
         // the ring's order: K of the first `ahead` tiles, then V of a tile and K
         // of the tile `ahead` after it; alternating streams take every other tile
         const int ahead = paired ? 1 : 2;
-        const bool every = paired || C::kGroups == 1;
-        for (int t = 0; t < min(ahead, n); ++t) {
-          if (every || t == g) {
-            take(cur, k_slots);
-            if (!ok) break;
-            tc_fence_after();
-            next_buf = -1;
-            if (elect_one()) qk(paired ? g : t, cur);
-            __syncwarp();
+        // A warp follows the ring over the tiles that are not its stream's, too:
+        // running ahead it would take an old filling of a slot for a later one.
+        // (It lets them go behind its own MMAs: the producers count on slots
+        // becoming free in the ring's order.)
+        auto pass = [&](int m) {
+          take(cur, m);
+          if (ok && elect_one()) release(cur, m);
+          __syncwarp();
+          cur.skip(m);
+        };
+        if (g == 1 && !turns) {
+          // nothing here for this stream: its softmax warps wait for this, so
+          // that they do not run ahead either
+          for (int t = 0; t < min(ahead, n) && ok; ++t) pass(k_slots);
+          for (int t = 0; t < n && ok; ++t) {
+            pass(C::kVSlots);
+            if (t + ahead < n) pass(k_slots);
           }
+          if (lane == 0) mbar_arrive(s_full(1));
+          continue;
+        }
+        const bool every = paired || C::kGroups == 1;
+        for (int t = 0; t < min(ahead, n) && ok; ++t) {
+          if (!every && t != g) {
+            pass(k_slots);
+            continue;
+          }
+          take(cur, k_slots);
+          if (!ok) break;
+          tc_fence_after();
+          next_buf = -1;
+          if (elect_one()) qk(paired ? g : t, cur);
+          __syncwarp();
           cur.skip(k_slots);
         }
         for (int t = 0; t < n && ok; ++t) {
           const bool more = t + ahead < n;
+          if (!every && (t & 1) != g) {
+            pass(C::kVSlots);
+            if (more) pass(k_slots);
+            continue;
+          }
           Pos nk = cur;
           nk.skip(C::kVSlots);
-          if (every || (t & 1) == g) {
-            const int buf = paired ? g : t & 1;
-            // the first product of all, and every one of a stream alone
-            if ((!turns || (t == 0 && g == 0)) && lane == 0) mbar_arrive(p_full(buf));
-            next_buf = !turns ? -1 : paired ? (g == 0 ? 1 : more ? 0 : -1) : t + 1 < n ? buf ^ 1 : -1;
-            take(cur, C::kVSlots);
-            if (more && C::kGroups == 2) take(nk, k_slots);
-            ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.status);
-            p_par ^= 1u << buf;
+          const int buf = paired ? g : t & 1;
+          // the first product of all, and every one of a stream alone
+          if ((!turns || (t == 0 && g == 0)) && lane == 0) mbar_arrive(p_full(buf));
+          next_buf = !turns ? -1 : paired ? (g == 0 ? 1 : more ? 0 : -1) : t + 1 < n ? buf ^ 1 : -1;
+          take(cur, C::kVSlots);
+          if (more && C::kGroups == 2) take(nk, k_slots);
+          ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.status);
+          p_par ^= 1u << buf;
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            pv(buf, cur, paired || C::kGroups == 1 ? t == 0 : t < 2);
+            if (more && C::kGroups == 2) qk(buf, nk);
+            else if (next_buf >= 0) mbar_arrive(p_full(next_buf));
+          }
+          __syncwarp();
+          if (more && C::kGroups == 1) {  // (the ring holds less than two tiles)
+            take(nk, k_slots);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-              pv(buf, cur, paired || C::kGroups == 1 ? t == 0 : t < 2);
-              if (more && C::kGroups == 2) qk(buf, nk);
-              else if (next_buf >= 0) mbar_arrive(p_full(next_buf));
-            }
+            next_buf = -1;
+            if (elect_one()) qk(buf, nk);
             __syncwarp();
-            if (more && C::kGroups == 1) {  // (the ring holds less than two tiles)
-              take(nk, k_slots);
-              if (!ok) break;
-              tc_fence_after();
-              next_buf = -1;
-              if (elect_one()) qk(buf, nk);
-              __syncwarp();
-            }
           }
           cur = nk;
           if (more) cur.skip(k_slots);
@@ -479,7 +501,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;  // tensor memory lane field
     const float c = a.scale_log2;
     uint32_t s_par = 0;  // parity of buffer b's scores: bit b
-    int o_cnt = 0;       // products of this stream
+    uint32_t o_par = 0;  // parity of the next product's phase on o_full(i): bit i
+    int o_last = 0;      // barrier of the last product
     bool ok = true;
     while (ok && run.next()) {
       const int h = run.unit / p.row_blocks;
@@ -612,7 +635,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           }
           if (any) {
             // O *= f, after the product that is under way
-            ok = wait_warp(o_full(g), (o_cnt - 1) & 1, &abort_s, a.status);
+            ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.status);
             if (!ok) break;
             tc_fence_after();
             l *= f;
@@ -642,7 +665,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           l += u + v;
         }
         any = true;
-        ++o_cnt;
+        o_last = C::kGroups == 2 ? g : b;
+        o_par ^= 1u << o_last;
       }
       if (ok && C::kGroups == 2 && g == 1 && (idle || (!paired && run.n < 2))) {
         ok = wait_warp(s_full(1), s_par >> 1 & 1u, &abort_s, a.status);
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
 
       // the unit's partial: O / l and the log of its weight
       if (any) {
-        ok = wait_warp(o_full(g), (o_cnt - 1) & 1, &abort_s, a.status);
+        ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.status);
         if (!ok) break;
         tc_fence_after();
       }
