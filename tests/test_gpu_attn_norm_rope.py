@@ -73,6 +73,14 @@ def test_norm_types(oracle_lib, xt, rt, wt, ot):
     _check_norm(5, 321, xt, rt, wt, ot, 0, seed=2)
 
 
+# rows of odd widths one behind the other: each row begins at another place between two vectors
+@pytest.mark.parametrize("d", [3, 9, 15, 250, 255, 1019, 1419, 2035, 2049, 4083, 4426, 8185, 16371, 16383])
+@pytest.mark.parametrize("xt,rt,wt,ot", [(F, F, F, Q), (B, F, B, B), (H, H, F, Q), (F, B, H, H)])
+def test_norm_odd_rows(oracle_lib, d, xt, rt, wt, ot):
+    _check_norm(17, d, xt, rt, wt, ot, 0, seed=d)
+    _check_norm(17, d, xt, rt, wt, ot, 0, x_pad=16, out_pad=8, seed=d)
+
+
 @pytest.mark.parametrize("d,group", [(64, 64), (128, 128), (192, 64), (2048, 128), (4096, 64),
                                      (16384, 64), (16384, 128), (640, 128)])
 @pytest.mark.parametrize("out_pad", [0, 3])
@@ -190,6 +198,23 @@ def test_rope_heads(oracle_lib, D, rot, style):
 @pytest.mark.parametrize("layout", ["nhd", "hnd"])
 def test_rope_lengths(oracle_lib, T, layout):
     _check_rope(T, 5, 1, 64, 64, 0, H, page=32, layout=layout, gap=24, seed=T)
+
+
+def test_norm_huge_values_keep_their_codes(oracle_lib):
+    """Maxima near the end of fp32's range: their reciprocals are small, not zero."""
+    x = torch.zeros(2, 128, device="cuda")
+    x[0, 0], x[1, :2] = 1.0, 1.0
+    w = torch.full((128,), 2.0 ** 123, device="cuda")
+    w[1] = 2.0 ** 122
+    out, scales = torch.empty(2, 128, dtype=Q, device="cuda"), torch.empty(2, 1, device="cuda")
+    dims = lily.make_norm_dims(2, 128, F, F, F, Q, eps=0.0)
+    lily.lily_attn_add_rmsnorm(dims, x, None, w, None, out, scales)
+    torch.cuda.synchronize()
+    # rows' norms: sqrt(128) and 8 times w, the largest above 2^126
+    codes = out.float().cpu()
+    assert codes[0, 0] == 448 and codes[1, 0] == 448 and codes[1, 1] == 224 and not codes[:, 2:].any()
+    top = torch.tensor([math.sqrt(128.0), 8.0], dtype=torch.float64) * 2.0 ** 123 / 448
+    assert ((scales[:, 0].cpu().double() - top).abs() <= 8 * 2.0 ** -24 * top).all()
 
 
 def test_rope_far_positions(oracle_lib):

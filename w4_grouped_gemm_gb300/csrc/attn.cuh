@@ -26,8 +26,7 @@ struct NormArgs {
   int T, d, xt, rt, wt, ot, group;
   float eps;
 };
-// vec: rows start on 8-element boundaries of every operand and d is a multiple of 8.
-cudaError_t launch_add_rmsnorm(const NormArgs& a, bool vec, cudaStream_t s);
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- rope + append
 struct RopeArgs {

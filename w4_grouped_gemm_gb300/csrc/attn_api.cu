@@ -234,11 +234,7 @@ int lily_attn_add_rmsnorm(const lily_attn_norm_dims* dims, const void* x, const 
   a.ot = d.out_dtype;
   a.group = d.group;
   a.eps = d.eps;
-  auto whole = [](int64_t stride, int type) { return stride * bytes_of(type) % (8 * (type == LILY_DTYPE_E4M3 ? 1 : 2)) == 0; };
-  const bool vec = d.d % 8 == 0 && whole(d.x_stride, d.x_dtype) && whole(d.out_stride, d.out_dtype) &&
-                   (!residual || whole(d.res_stride, d.res_dtype)) &&
-                   (!residual_out || whole(d.res_out_stride, d.res_dtype));
-  return rc_of(launch_add_rmsnorm(a, vec, (cudaStream_t)stream));
+  return rc_of(launch_add_rmsnorm(a, (cudaStream_t)stream));
 }
 
 int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache* cache,

@@ -8,12 +8,15 @@
 // of its groups and its stores, so that x and the residual are read once and
 // the outputs written once.  HBM bounds it from some hundred rows on, the
 // latency of one load and two block reductions below.
+#include <climits>
 #include <cuda_fp8.h>
 
 #include "attn.cuh"
 
 namespace lily {
 namespace {
+
+constexpr int kMaxWarps = 16;  // of a block
 
 // Raw bits of eight consecutive elements: 16-bit types use a, fp32 a and b.
 // Loading the bits first and converting later keeps a row's loads of both
@@ -69,55 +72,91 @@ __device__ __forceinline__ float load1(const void* p, int64_t i, int type) {
   return lo16_f32(static_cast<const uint16_t*>(p)[i], type == LILY_DTYPE_F16);
 }
 
+__device__ __forceinline__ void store1(void* p, int64_t i, float v, int type) {
+  if (type == LILY_DTYPE_F32) static_cast<float*>(p)[i] = v;
+  else static_cast<uint16_t*>(p)[i] = pack1(v, type == LILY_DTYPE_F16);
+}
+
 __device__ __forceinline__ uint16_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 
-// Sum over the WPR warps of a row (tmp: one float per warp of the block).
-// fmaxf drops a NaN, so NaN reaches the scales through the norm's factor
-// instead (see below).
-template <int WPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* tmp) {
+// Sum over the warps of a row: WPR of them, or the whole block (0).  tmp: a
+// float per warp of the block.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* tmp) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, u) : v + u;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (WPR == 1) return v;
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) tmp[warp] = v;
   __syncthreads();
-  const int first = warp / WPR * WPR;
+  if (WPR == 0) {
+    const int lane = threadIdx.x & 31;
+    v = lane < (int)blockDim.x >> 5 ? tmp[lane] : 0.f;
+#pragma unroll
+    for (int o = kMaxWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return __shfl_sync(0xffffffffu, v, 0);
+  }
+  const int first = warp / (WPR ? WPR : 1) * WPR;
   v = tmp[first];
 #pragma unroll
-  for (int w = 1; w < WPR; ++w) v = MAX ? fmaxf(v, tmp[first + w]) : v + tmp[first + w];
+  for (int w = 1; w < WPR; ++w) v += tmp[first + w];
   return v;
 }
 
-// A row on WPR warps, C chunks of eight elements per thread.  VEC: chunk c of
-// thread t covers columns 8 (c*threads + t) .. +7; else its elements are the
-// columns (8c + e)*threads + t, one at a time (any alignment).
+// r[e] *= f * w for the columns O before a boundary of eight: w[0..7] are the
+// weights of the eight columns before it, w[8..15] those from it on.
+template <int O>
+__device__ __forceinline__ void scale8(float (&r)[8], const float (&w)[16], float f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] *= f * w[8 - O + e];
+}
+
+// How a row's elements lie on its threads, C chunks of eight per thread:
+//   kWhole: chunk c of thread t covers columns 8 (c*threads + t) .. +7
+//   kShift: the same, less the row's first element's distance from a boundary
+//     of eight (rows of odd widths one behind the other: every operand of a
+//     row has the same distance).  The first and last chunk's vectors reach
+//     into the neighbouring rows, whose elements count as zeros and are not
+//     written; only past the last row are they loaded one by one.  The
+//     weights, which have no distance, come as two vectors and a uniform
+//     choice of eight shifts.  (10394 fp32 rows of 4426 into 8 bits: 113 us;
+//     element by element 293.)
+//   kAny: columns (8c + e)*threads + t, one at a time
+enum Lay { kAny, kWhole, kShift };
+
+// A row on WPR warps, or on a block of as many warps as its chunks need (0).
+// (Eight warps known when compiling take 82 us for 16384 rows of 4096 in bf16,
+// out in 8 bits; as a block of any size 90.)
 // XT, RT, OT: element types known when compiling, -1: asked at run time (OT 0:
 // one of the 16-bit types).  Asked at run time they cost half of the issue
 // slots, which then bound the kernel (16384 rows of 4096 into 8 bits: 93 us).
-template <int WPR, int C, bool VEC, int XT, int RT, int OT>
-__global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
+template <int WPR, int C, Lay LAY, int XT, int RT, int OT>
+__global__ void __launch_bounds__(WPR ? 256 : 32 * kMaxWarps)
     add_rmsnorm_kernel(const NormArgs a) {
-  constexpr int kTPR = WPR * 32;
-  constexpr int kThreads = kTPR > 256 ? kTPR : 256;
-  constexpr int kRows = kThreads / kTPR;
+  constexpr bool VEC = LAY != kAny;
+  constexpr int kRows = WPR ? 8 / WPR : 1;  // rows of a block
+  const int kThreads = WPR ? 256 : blockDim.x, kTPR = WPR ? WPR * 32 : blockDim.x;
   const int xt = XT >= 0 ? XT : a.xt, rt = RT >= 0 ? RT : a.rt;
   const bool bits8 = OT >= 0 ? OT == LILY_DTYPE_E4M3 : a.ot == LILY_DTYPE_E4M3;
-  __shared__ float tmp[2][kThreads / 32];
+  __shared__ float tmp[2][kMaxWarps];
   __shared__ uint32_t gmax[VEC ? 1 : kRows][VEC ? 1 : 256];  // element-wise groups: bits of the maxima
 
   const int t = threadIdx.x % kTPR;
   const int sub = threadIdx.x / kTPR;
   const int64_t row = (int64_t)blockIdx.x * kRows + sub;
   const bool live = row < a.T;
-  auto col = [&](int c, int e) { return VEC ? 8 * (c * kTPR + t) + e : (8 * c + e) * kTPR + t; };
+  const int shift = LAY == kShift ? (int)(row * a.x_stride & 7) : 0;
+  auto col = [&](int c, int e) { return VEC ? 8 * (c * kTPR + t) + e - shift : (8 * c + e) * kTPR + t; };
+  auto inside = [&](int c, int e) { return col(c, e) >= 0 && col(c, e) < a.d; };
+  auto some = [&](int c) { return live && col(c, 0) < a.d && (LAY != kShift || col(c, 7) >= 0); };
+  auto whole = [&](int c) { return LAY != kShift || (col(c, 0) >= 0 && col(c, 7) < a.d); };
+  // columns from this row's first on that are there in every operand
+  const int there = LAY == kShift ? (int)min((int64_t)(a.T - row) * a.d, (int64_t)INT_MAX) : 0;
+  auto vectors = [&](int c) { return some(c) && (LAY != kShift || col(c, 7) < there); };
 
   pdl_wait();
   pdl_trigger();
@@ -128,19 +167,30 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
     Raw8 rx[C], rr[C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (live && col(c, 0) < a.d) {
+      if (vectors(c)) {
         load_raw8(rx[c], a.x, xi + col(c, 0), xt);
         if (a.res) load_raw8(rr[c], a.res, ri + col(c, 0), rt);
       }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (live && col(c, 0) < a.d) {
+      if (LAY == kShift && some(c) && !vectors(c)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          r[c][e] = inside(c, e) ? load1(a.x, xi + col(c, e), xt) +
+                                       (a.res ? load1(a.res, ri + col(c, e), rt) : 0.f)
+                                 : 0.f;
+      } else if (some(c)) {
         unpack8(rx[c], xt, r[c]);
         if (a.res) {
           float v[8];
           unpack8(rr[c], rt, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) r[c][e] += v[e];
+        }
+        if (!whole(c)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!inside(c, e)) r[c][e] = 0.f;
         }
       } else {
 #pragma unroll
@@ -166,15 +216,19 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(r[c][e], r[c][e], ss);
-  ss = row_reduce<WPR, false>(ss, tmp[0]);
+  ss = row_sum<WPR>(ss, tmp[0]);
   const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
 
   // the rounded residual leaves, and r becomes n
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (VEC) {
-      if (!(live && col(c, 0) < a.d)) continue;
-      if (a.res_out) {
+      if (!some(c)) continue;
+      if (LAY == kShift && a.res_out && !whole(c)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (inside(c, e)) store1(a.res_out, row * a.res_out_stride + col(c, e), r[c][e], rt);
+      } else if (a.res_out) {
         const int64_t o = row * a.res_out_stride + col(c, 0);
         if (rt == LILY_DTYPE_F32) {
           float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.res_out) + o);
@@ -185,11 +239,43 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
               pack8(r[c], rt == LILY_DTYPE_F16);
         }
       }
-      if (a.w) {
+      if (a.w && LAY == kShift && shift) {
+        float w[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int at = col(c, 0) + shift - 8 + 8 * k;
+          float v[8];
+          if (at >= 0 && at + 8 <= a.d) {
+            Raw8 raw;
+            load_raw8(raw, a.w, at, a.wt);
+            unpack8(raw, a.wt, v);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = at + e >= 0 && at + e < a.d ? load1(a.w, at + e, a.wt) : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[8 * k + e] = v[e];
+        }
+        switch (shift) {
+          case 1: scale8<1>(r[c], w, rstd); break;
+          case 2: scale8<2>(r[c], w, rstd); break;
+          case 3: scale8<3>(r[c], w, rstd); break;
+          case 4: scale8<4>(r[c], w, rstd); break;
+          case 5: scale8<5>(r[c], w, rstd); break;
+          case 6: scale8<6>(r[c], w, rstd); break;
+          default: scale8<7>(r[c], w, rstd);
+        }
+      } else if (a.w) {  // (in the first row of kShift the last chunk may be partial)
         float w[8];
-        Raw8 rw;
-        load_raw8(rw, a.w, col(c, 0), a.wt);
-        unpack8(rw, a.wt, w);
+        if (LAY == kShift && col(c, 7) >= a.d) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = inside(c, e) ? load1(a.w, col(c, e), a.wt) : 0.f;
+        } else {
+          Raw8 rw;
+          load_raw8(rw, a.w, col(c, 0), a.wt);
+          unpack8(rw, a.wt, w);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] *= rstd * w[e];
       } else {
@@ -200,11 +286,7 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (!(live && col(c, e) < a.d)) continue;
-        if (a.res_out) {
-          const int64_t o = row * a.res_out_stride + col(c, e);
-          if (rt == LILY_DTYPE_F32) static_cast<float*>(a.res_out)[o] = r[c][e];
-          else static_cast<uint16_t*>(a.res_out)[o] = pack1(r[c][e], rt == LILY_DTYPE_F16);
-        }
+        if (a.res_out) store1(a.res_out, row * a.res_out_stride + col(c, e), r[c][e], rt);
         r[c][e] *= a.w ? rstd * load1(a.w, col(c, e), a.wt) : rstd;
       }
     }
@@ -215,13 +297,12 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
     uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_stride;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (VEC) {
-        if (live && col(c, 0) < a.d)
-          *reinterpret_cast<uint4*>(out + col(c, 0)) = pack8(r[c], h);
-      } else {
+      if (VEC && some(c) && whole(c)) {
+        *reinterpret_cast<uint4*>(out + col(c, 0)) = pack8(r[c], h);
+      } else if (!VEC || (LAY == kShift && some(c))) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (live && col(c, e) < a.d) out[col(c, e)] = pack1(r[c][e], h);
+          if (live && inside(c, e)) out[col(c, e)] = pack1(r[c][e], h);
       }
     }
     return;
@@ -244,12 +325,18 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 #pragma unroll
     for (int c = 1; c < C; ++c) m[0] = max(m[0], m[c]);
     m[0] = __reduce_max_sync(0xffffffffu, m[0]);
-    if (WPR > 1) {
-      const int warp = threadIdx.x >> 5, first = warp / WPR * WPR;
-      if ((threadIdx.x & 31) == 0) tmp[1][warp] = __uint_as_float(m[0]);
+    if (WPR != 1) {
+      const int warp = threadIdx.x >> 5;
+      const int lane = threadIdx.x & 31;
+      if (lane == 0) tmp[1][warp] = __uint_as_float(m[0]);
       __syncthreads();
+      if (WPR == 0) {
+        m[0] = __reduce_max_sync(0xffffffffu, lane < (int)blockDim.x >> 5 ? __float_as_uint(tmp[1][lane]) : 0u);
+      } else {
+        const int first = warp / (WPR ? WPR : 1) * WPR;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) m[0] = max(m[0], __float_as_uint(tmp[1][first + w]));
+        for (int w = 0; w < WPR; ++w) m[0] = max(m[0], __float_as_uint(tmp[1][first + w]));
+      }
     }
 #pragma unroll
     for (int c = 1; c < C; ++c) m[c] = m[0];
@@ -276,29 +363,34 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 
   float* sc = a.scales + row * n_groups;
   uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
-  // n / s as n * (448 / max); where that would not be a normal number, divided
-  // (the last bits of the quotient are lost in e4m3's rounding, and the largest
-  // value still lands on 448)
+  // n / s as n * (448 / max), both rounded to 32 bits like s and the quotient;
+  // where 448 / max would not be a normal number, divided
   constexpr float kTiny = 1e-30f, kStep = 1.f / 448.f;
   if (per_row && t == 0) sc[0] = __uint_as_float(m[0]) * kStep;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     if (VEC) {
-      if (col(c, 0) >= a.d) continue;
+      if (!some(c)) continue;
       const float top = __uint_as_float(m[c]), s = top * kStep;
       if (!per_row && (col(c, 0) & (a.group - 1)) == 0) sc[col(c, 0) / a.group] = s;
       if (s > 0.f && s < kTiny) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] / s;
       } else {
-        const float inv = top == 0.f ? 0.f : __fdividef(448.f, top);
+        const float inv = top == 0.f ? 0.f : 448.f / top;
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] *= inv;
       }
       uint2 o;
       o.x = e4m3x2(r[c][0], r[c][1]) | (uint32_t)e4m3x2(r[c][2], r[c][3]) << 16;
       o.y = e4m3x2(r[c][4], r[c][5]) | (uint32_t)e4m3x2(r[c][6], r[c][7]) << 16;
-      *reinterpret_cast<uint2*>(out + col(c, 0)) = o;
+      if (whole(c)) {
+        *reinterpret_cast<uint2*>(out + col(c, 0)) = o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (inside(c, e)) out[col(c, e)] = (uint8_t)((e < 4 ? o.x : o.y) >> (8 * (e & 3)));
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -314,41 +406,63 @@ __global__ void __launch_bounds__(WPR * 32 > 256 ? WPR * 32 : 256)
 }
 
 template <int WPR, int C, int XT, int RT, int OT>
-cudaError_t launch_types(const NormArgs& a, bool vec, cudaStream_t s) {
-  constexpr int kThreads = WPR * 32 > 256 ? WPR * 32 : 256;
-  constexpr int kRows = kThreads / (WPR * 32);
-  const unsigned grid = (unsigned)(((int64_t)a.T + kRows - 1) / kRows);
-  if (XT < 0 && !vec)
-    return launch_pdl(add_rmsnorm_kernel<WPR, C, false, -1, -1, -1>, dim3(grid), dim3(kThreads), 0, s, a);
-  return launch_pdl(add_rmsnorm_kernel<WPR, C, true, XT, RT, OT>, dim3(grid), dim3(kThreads), 0, s, a);
+cudaError_t launch_types(const NormArgs& a, Lay lay, int chunks, cudaStream_t s) {
+  constexpr int kRows = WPR ? 8 / WPR : 1;
+  const dim3 grid((unsigned)(((int64_t)a.T + kRows - 1) / kRows));
+  const dim3 threads(WPR ? 256 : (chunks + 32 * C - 1) / (32 * C) * 32);
+  if (XT < 0 && lay == kAny)
+    return launch_pdl(add_rmsnorm_kernel<WPR, C, kAny, -1, -1, -1>, grid, threads, 0, s, a);
+  if (WPR != 8 && lay == kShift)
+    return launch_pdl(add_rmsnorm_kernel<WPR, C, WPR == 8 ? kWhole : kShift, XT, RT, OT>, grid, threads, 0, s, a);
+  return launch_pdl(add_rmsnorm_kernel<WPR, C, kWhole, XT, RT, OT>, grid, threads, 0, s, a);
 }
 // The types of one kind throughout, with an fp32 residual or without one, are
 // compiled in; other mixtures, and rows of any alignment, ask at run time.
 template <int WPR, int C>
-cudaError_t launch_as(const NormArgs& a, bool vec, cudaStream_t s) {
+cudaError_t launch_as(const NormArgs& a, Lay lay, int n8, cudaStream_t s) {
   constexpr int B = LILY_DTYPE_BF16, H = LILY_DTYPE_F16, F = LILY_DTYPE_F32, Q = LILY_DTYPE_E4M3;
   const bool q = a.ot == Q;
-  if (vec && (a.rt == F || a.rt == a.xt)) {
-    if (a.xt == B && a.rt == B) return q ? launch_types<WPR, C, B, B, Q>(a, vec, s) : launch_types<WPR, C, B, B, 0>(a, vec, s);
-    if (a.xt == B) return q ? launch_types<WPR, C, B, F, Q>(a, vec, s) : launch_types<WPR, C, B, F, 0>(a, vec, s);
-    if (a.xt == H && a.rt == H) return q ? launch_types<WPR, C, H, H, Q>(a, vec, s) : launch_types<WPR, C, H, H, 0>(a, vec, s);
-    if (a.xt == H) return q ? launch_types<WPR, C, H, F, Q>(a, vec, s) : launch_types<WPR, C, H, F, 0>(a, vec, s);
-    return q ? launch_types<WPR, C, F, F, Q>(a, vec, s) : launch_types<WPR, C, F, F, 0>(a, vec, s);
+  if (lay != kAny && (a.rt == F || a.rt == a.xt)) {
+    if (a.xt == B && a.rt == B) return q ? launch_types<WPR, C, B, B, Q>(a, lay, n8, s) : launch_types<WPR, C, B, B, 0>(a, lay, n8, s);
+    if (a.xt == B) return q ? launch_types<WPR, C, B, F, Q>(a, lay, n8, s) : launch_types<WPR, C, B, F, 0>(a, lay, n8, s);
+    if (a.xt == H && a.rt == H) return q ? launch_types<WPR, C, H, H, Q>(a, lay, n8, s) : launch_types<WPR, C, H, H, 0>(a, lay, n8, s);
+    if (a.xt == H) return q ? launch_types<WPR, C, H, F, Q>(a, lay, n8, s) : launch_types<WPR, C, H, F, 0>(a, lay, n8, s);
+    return q ? launch_types<WPR, C, F, F, Q>(a, lay, n8, s) : launch_types<WPR, C, F, F, 0>(a, lay, n8, s);
   }
-  return launch_types<WPR, C, -1, -1, -1>(a, vec, s);
+  return launch_types<WPR, C, -1, -1, -1>(a, lay, n8, s);
 }
 
 }  // namespace
 
-cudaError_t launch_add_rmsnorm(const NormArgs& a, bool vec, cudaStream_t s) {
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
+  // What the rows' addresses allow (the bases lie on 16 bytes).
+  int64_t all[4] = {a.x_stride, a.out_stride, a.res ? a.res_stride : a.x_stride,
+                    a.res_out ? a.res_out_stride : a.x_stride};
+  const int types[4] = {a.xt, a.ot, a.rt, a.rt};
+  bool same = a.group == 0, whole = a.d % 8 == 0;
+  for (int i = 0; i < 4; ++i) {
+    if (a.T == 1) all[i] = 0;  // (no second row)
+    whole = whole && all[i] % (types[i] == LILY_DTYPE_F32 ? 4 : 8) == 0;
+    same = same && (all[i] - all[0]) % 8 == 0;
+  }
+  int n8 = (a.d + 7) / 8;  // chunks of a row
+  Lay lay = kAny;
+  if (whole) {
+    lay = kWhole;
+  } else if (same && (a.d + 14) / 8 <= 2048) {
+    lay = kShift;
+    n8 = (a.d + 14) / 8;
+  }
   prof_begin(K_ATTN_NORM, s);
-  const int n8 = (a.d + 7) / 8;  // chunks of a row
   cudaError_t e;
-  if (n8 <= 32) e = launch_as<1, 1>(a, vec, s);
-  else if (n8 <= 128) e = launch_as<4, 1>(a, vec, s);
-  else if (n8 <= 256) e = launch_as<8, 1>(a, vec, s);
-  else if (n8 <= 512) e = launch_as<8, 2>(a, vec, s);
-  else e = launch_as<16, 4>(a, vec, s);
+  if (n8 <= 32) e = launch_as<1, 1>(a, lay, n8, s);
+  else if (n8 <= 128) e = launch_as<4, 1>(a, lay, n8, s);
+  else if (lay == kWhole && n8 > 224 && n8 <= 256) e = launch_as<8, 1>(a, lay, n8, s);
+  else if (lay == kWhole && n8 > 448 && n8 <= 512) e = launch_as<8, 2>(a, lay, n8, s);
+  // (kShift holds the weights of a chunk twice: one chunk per thread where that does)
+  else if (n8 <= (lay == kShift ? 512 : 256)) e = launch_as<0, 1>(a, lay, n8, s);
+  else if (n8 <= 1024) e = launch_as<0, 2>(a, lay, n8, s);
+  else e = launch_as<0, 4>(a, lay, n8, s);
   prof_end(K_ATTN_NORM, s);
   return e;
 }
