@@ -8,8 +8,8 @@
 namespace lily {
 namespace {
 
-// A query row (token, query head) per W warps, 8 / W rows per block (W 32: one
-// row in a block of 32 warps): the
+// A query row (token, query head) per W warps, 8 / W rows per block (W 16 and
+// 32: one row in a block of W warps): the
 // partials of the prefix and of the sequence's own keys, weighted by 2^(lse -
 // largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
 // finds the weight of one of them, then all lanes add up their outputs, up to
@@ -20,7 +20,7 @@ namespace {
 // counts where its sequence has the row's token and keys, for then this call
 // has written it.
 template <int W>
-__global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 1 : 4)
+__global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : 4)
     attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
   constexpr int kWarps = W > 8 ? W : 8, kRows = kWarps / W;  // of a block
   __shared__ __align__(16) float acc_s[W > 1 ? kWarps : 1][W > 1 ? 256 : 4];
@@ -211,25 +211,29 @@ cudaError_t launch_attn_keys(const AttnArgs& a, const AttnSet& pa, const AttnSet
 
 cudaError_t launch_attn_merge(const AttnArgs& a, const MergeArgs& m, cudaStream_t s) {
   prof_begin(K_ATTN_MERGE, s);
-  // Warps for a row: one per four partials (the prefix's are known here, a
-  // sequence's own lengths only on the device), more where rows are too few to
-  // give every SM two blocks.
-  int n = 1;
+  // Warps for a row: one per two to four partials (the prefix's are known here;
+  // a sequence's own, whose lengths only the device knows, are taken as if all
+  // were the longest), as long as all rows' warps find a place on the GPU at
+  // once: 1000 rows of 33 partials took 23.6 us of a call with 4 warps each,
+  // 26.2 with 8 and 53.5 with 32; 256 rows of 67, 23.1 with 8, 21.8 with 16 and
+  // 27.0 with 32; 16 rows of 17, 17.7 with 1, 12.1 with 8.
+  int n = 0;
   if (m.pre_tiles) n += (m.pre_tiles / m.pre_share + 2) * m.pre_streams;
+  if (m.own.rows_at) n += 1 + m.own_parts;
   const int64_t rows = (int64_t)a.T * a.hq;
   int w = 1;
-  while (w < 8 && (n > 4 * w || (n >= 2 * w && rows * w < 8 * 2 * 152))) w *= 2;
-  if (n > 32) w = 32;
+  while (w < 32 && n > (rows * w < 8 * 152 ? 2 : 4) * w && rows * 2 * w <= 4096) w *= 2;
   const int per = w > 8 ? 1 : 8 / w;
   const dim3 grid((unsigned)((rows + per - 1) / per));
   auto launch = [&](auto kern) {
     return launch_pdl(kern, grid, dim3(w > 8 ? 32 * w : 256), 0, s, a, m);
   };
-  const cudaError_t e = w == 1   ? launch(attn_merge_kernel<1>)
-                        : w == 2 ? launch(attn_merge_kernel<2>)
-                        : w == 4 ? launch(attn_merge_kernel<4>)
-                        : w == 8 ? launch(attn_merge_kernel<8>)
-                                 : launch(attn_merge_kernel<32>);
+  const cudaError_t e = w == 1    ? launch(attn_merge_kernel<1>)
+                        : w == 2  ? launch(attn_merge_kernel<2>)
+                        : w == 4  ? launch(attn_merge_kernel<4>)
+                        : w == 8  ? launch(attn_merge_kernel<8>)
+                        : w == 16 ? launch(attn_merge_kernel<16>)
+                                  : launch(attn_merge_kernel<32>);
   prof_end(K_ATTN_MERGE, s);
   return e;
 }

@@ -68,9 +68,14 @@ int check_attn_dims(const lily_attn_dims* d, const lily_attn_cache* c) {
 // Rows per unit: 8, 16, 32 or 64, the least that holds `rows` (64 at most).
 int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// Query rows per KV head from which the prefix goes to the tensor-core kernel:
-// above one mma.sync row block.
+// The prefix goes to the tensor-core kernel where it has more rows per KV head
+// than one mma.sync row block (above, both read it once) and enough tiles of 64
+// rows and keys for that kernel's launch, its load of Q and its larger partials
+// to pay (128 sequences of 8 rows on one KV head, D = 128: 15.9 against 17.3 us
+// at 256 tiles, 14.9 against 14.4 at 64; D = 256: 23.3 against 20.6 at 256, 24.8
+// against 29.4 at 512; 4 heads of 250 rows, D = 128: 28.6 against 47.3 at 4096).
 constexpr int kTcRows = 64;
+constexpr int tc_tiles(int D) { return D <= 128 ? 256 : 512; }
 
 // What a call launches, and its workspace: the status word, then the two sets'
 // partials and the own set's runs.  Sized for the largest grid, so that it
@@ -110,7 +115,7 @@ bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   };
   if (d.prefix_len) {
     const int64_t rows = (int64_t)d.n_tokens * G;
-    p.tc = rows > kTcRows;
+    p.tc = rows > kTcRows && c.n_kv_heads * ((rows + 63) / 64) * ((d.prefix_len + 63) / 64) >= tc_tiles(c.head_dim);
     if (p.tc) {
       TcArgs& t = p.ptc;
       t.paired = rows > 128 && c.head_dim <= 128;
@@ -418,6 +423,8 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     o.rows_at = reinterpret_cast<int4*>(base + p.rows_at);
     o.grid = own_grid;
     m.own = o;
+    m.own_parts = (int)((d.max_seq_len + kAttnTile - 1) / kAttnTile /
+                        ((p.own_most + own_grid - 1) / own_grid));
   }
   // the sets that mma.sync takes, in one launch
   if (p.pre.grid + p.own.grid) {

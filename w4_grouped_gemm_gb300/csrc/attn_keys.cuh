@@ -41,7 +41,7 @@ struct Cfg {
   static constexpr int kWK = kWarps / WR;        // warps that split a tile's keys
   static constexpr int kKeys = kTile / kWK;      // keys of a warp
   static constexpr int kOcc = DP <= 128 ? 2 : 1;
-  static constexpr int kStages = DP == 64 ? 6 : 3;
+  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 2 : 3;
   static constexpr int kHalfBytes = kTile * 128;             // 64 keys x 64 dimensions
   static constexpr int kTileBytes = kHalfBytes * (DP / 64);  // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;

@@ -296,17 +296,23 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           // would reach every row: it is set to zero before the MMAs see it
           if (!(ok = wait_warp(land, land_par, &abort_s, a.status))) return;
           land_par ^= 1;
-          for (int k = 0; k < kKeys; ++k) {
-            if (__shfl_sync(0xffffffffu, w, (k >> 5) * 8) >> (k & 31) & 1u) continue;
+          // (a key per lane, its pieces in an order that spreads the lanes over
+          // the banks; key after key by the whole warp took 11 us of a short
+          // prefix's 25)
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) {
+            const int k = 32 * i + lane;
+            if (__shfl_sync(0xffffffffu, w, 8 * i) >> lane & 1u) continue;
             Pos z = cur;
             z.skip(k / C::kVKeys);
-            for (int x = lane; x < blocks * 8; x += 32)
+            const uint32_t at = slots + z.slot * C::kSlot + k % C::kVKeys * 128;
+            for (int x = 0; x < blocks * 8; ++x)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               slots + z.slot * C::kSlot +
-                               ((x >> 3) * C::kVKeys + k % C::kVKeys) * 128 + (x & 7) * 16),
+                               at + (x >> 3) * (C::kVKeys * 128) + ((x + lane) & 7) * 16),
                            "r"(0)
                            : "memory");
           }
+          __syncwarp();
           fence_proxy_async_smem();
           __syncwarp();
           if (active && in_slot == 0) mbar_arrive(full(mine.slot));
