@@ -13,14 +13,15 @@ namespace {
 // partials of the prefix and of the sequence's own keys, weighted by 2^(lse -
 // largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
 // finds the weight of one of them, then all lanes add up their outputs, up to
-// four at a time (eight took 122 registers, and the rows then waited for a place
-// on the SMs: 15 us for 8192 rows of one partial).  What bounds it is the chain of loads (where a row's own
+// four at a time, two where rows are many and partials few: what counts then is
+// rows in flight (13000 rows of two partials in a call: 52.4 us with four blocks
+// of 64 registers on an SM, 47.1 with five of 48, 49.6 with six that spill).  What bounds it is the chain of loads (where a row's own
 // partials lie, its sequence, lse, output), so the prefix's lse are requested
 // with the first.  rows_at may hold anything for rows without own keys: an entry
 // counts where its sequence has the row's token and keys, for then this call
 // has written it.
 template <int W>
-__global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : 4)
+__global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : W == 1 ? 5 : 4)
     attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
   constexpr int kWarps = W > 8 ? W : 8, kRows = kWarps / W;  // of a block
   __shared__ __align__(16) float acc_s[W > 1 ? kWarps : 1][W > 1 ? 256 : 4];
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : 4)
     const int cnt = min(32, (n - part - W * k0 + W - 1) / W);
     auto add = [&](auto wide) {
       constexpr int kWide = decltype(wide)::value;  // quads of columns per lane
-      constexpr int kAt = 4 / kWide;
+      constexpr int kAt = (W == 1 ? 2 : 4) / kWide;
       for (int j0 = 0; j0 < cnt; j0 += kAt) {
         float4 v[kAt][kWide];
         float w[kAt];

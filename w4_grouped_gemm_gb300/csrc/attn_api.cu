@@ -372,16 +372,8 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     // one tensor-core CTA per SM
     const int64_t sms = grid / (cache->head_dim <= 128 ? 2 : 1);
     const int64_t most = !p.tc ? pre_grid : sms < kTcMaxGrid ? sms : kTcMaxGrid;
-    int used = (int)(p.pre_total < most ? p.pre_total : most);
+    const int used = (int)(p.pre_total < most ? p.pre_total : most);
     m.pre_share = (int)((p.pre_total + used - 1) / used);
-    // A tensor-core CTA costs about six tiles of time besides its own, and the
-    // own pages' CTAs fill the SMs that it leaves: where these may take longer
-    // (64 MB are 10 us) fewer CTAs with six tiles each are the better share.
-    const int64_t own_bytes = p.own_most * kAttnTile * cache->head_dim * 4;
-    if (p.tc && m.pre_share < 6 && own_bytes > (int64_t)64 << 20) {
-      m.pre_share = p.pre_total < 6 ? (int)p.pre_total : 6;
-      used = (int)((p.pre_total + m.pre_share - 1) / m.pre_share);
-    }
     m.pre_o = part_o;
     m.pre_lse = part_lse;
     if (p.tc) {
