@@ -14,7 +14,7 @@ namespace {
 // largest lse) and added up.  Warp p of a row takes partials p, p + W, ..: a lane
 // finds the weight of one of them, then all lanes add up their outputs, up to
 // four at a time, two where rows are many and partials few: what counts then is
-// rows in flight (13000 rows of two partials in a call: 52.4 us with four blocks
+// rows in flight (26000 rows of two partials in a call: 52.4 us with four blocks
 // of 64 registers on an SM, 47.1 with five of 48, 49.6 with six that spill).  What bounds it is the chain of loads (where a row's own
 // partials lie, its sequence, lse, output), so the prefix's lse are requested
 // with the first.  rows_at may hold anything for rows without own keys: an entry

