@@ -24,7 +24,7 @@
 // behind the other's loads.
 //
 // Measured, in a graph, with the merge: 4 sequences behind 131072 keys (16 query
-// heads on 2, D = 256): 64 us, 270 MB, 4.2 TB/s; 96 sequences with up to 2500
+// heads on 2, D = 256): 58 us, 270 MB, 4.7 TB/s; 96 sequences with up to 2500
 // own keys behind 2051 (32 heads on 8, D = 128): 120 us, 540 MB, 4.5 TB/s; one
 // sequence of 301 keys: 8.9 us, of which the two launches and the merge are some
 // 6.  A CTA spends some 2 us on a unit besides its tiles (rows of Q, the warps'
