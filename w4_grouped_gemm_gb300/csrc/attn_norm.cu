@@ -367,7 +367,9 @@ __global__ void __launch_bounds__(WPR ? 256 : 32 * kMaxWarps)
   float* sc = a.scales + row * n_groups;
   uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
   // n / s as n * (448 / max), both rounded to 32 bits like s and the quotient;
-  // where 448 / max would not be a normal number, divided
+  // where 448 / max would not be a normal number, divided.  A maximum so small
+  // that s rounds to 0 gives 0, like one that is 0 (448 / max would be infinite
+  // there, and 0 times it NaN).
   constexpr float kTiny = 1e-30f, kStep = 1.f / 448.f;
   if (per_row && t == 0) sc[0] = __uint_as_float(m[0]) * kStep;
 #pragma unroll
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(WPR ? 256 : 32 * kMaxWarps)
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] / s;
       } else {
-        const float inv = top == 0.f ? 0.f : 448.f / top;
+        const float inv = s == 0.f ? 0.f : 448.f / top;
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] *= inv;
       }
