@@ -37,3 +37,44 @@ def test_norm_maximum_whose_scale_rounds_to_zero(oracle_lib, d, group, x_pad, ou
     assert bool((codes[1::2, 1:] == 448).all()) and bool((codes[1::2, 0] == 0).all())
     # (rows of ones: n = 1 to a few roundings of fp32)
     assert bool(((scales[1::2].double() * 448 - 1).abs() <= 2.0 ** -20).all())
+
+
+# ------------------------------------------------------------------------------------ rope, append
+def _turn(x, positions, rot, freq):
+    """Half-split rotation in 64 bits of x [T][heads][D]."""
+    x = x.double().clone()
+    angle = positions.double()[:, None, None] * freq
+    a, b = x[..., :rot // 2].clone(), x[..., rot // 2:rot].clone()
+    x[..., :rot // 2] = a * angle.cos() - b * angle.sin()
+    x[..., rot // 2:rot] = b * angle.cos() + a * angle.sin()
+    return x
+
+
+@pytest.mark.parametrize("rot", [20, 64])                # element by element; in vectors
+def test_rope_head_offsets_past_31_bits(oracle_lib, rot):
+    """Heads so far apart that a head's offset passes 2^31 elements: q and q_out, k and v lie in two
+    buffers, token by token behind one another within a head."""
+    T, heads, D = 3, 3, 64
+    stride = (1 << 31) - 8                               # elements, the largest that is taken
+    gen = torch.Generator().manual_seed(rot)
+    far = [torch.empty(2 * stride + 1024, dtype=B, device="cuda") for _ in range(2)]
+    q, q_out, k, v = (far[i // 2][512 * (i % 2):].as_strided((T, heads, D), (D, stride, 1))
+                      for i in range(4))
+    data = [torch.randn(T, heads, D, generator=gen).to(B) for _ in range(3)]
+    for at, x in zip((q, k, v), data):
+        at.copy_(x)
+    kc, vc = (torch.zeros(1, 16, heads, D, dtype=B, device="cuda") for _ in range(2))
+    pos = torch.tensor([5, 1000, 77], dtype=torch.int32)
+    freq = 1e4 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    ws = lily.alloc_workspace(256)
+    lily.lily_attn_rope_append(lily.make_rope_dims(q, k, v, q_out, rot), lily.PagedCache(kc, vc), q, k,
+                               v, pos.cuda(), torch.tensor([9, 0, 4], device="cuda"), freq.cuda(),
+                               q_out, ws)
+    torch.cuda.synchronize()
+    assert lily.lily_moe_status(ws) == 0
+    slots = [9, 0, 4]
+    for got, x in ((q_out, data[0]), (kc[0, slots], data[1])):
+        want = _turn(x, pos, rot, freq)
+        # bf16's rounding, and fp32 sines of both of a pair's elements (at most 6 in size)
+        assert bool(((got.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 12 * 2.0 ** -20).all())
+    assert torch.equal(vc[0, slots].cpu(), data[2])

@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a,
       const uint16_t* src;
       uint16_t* dst;
       if (h < a.hq) {
-        src = static_cast<const uint16_t*>(a.q) + t * a.q_tok + h * a.q_head;
-        dst = static_cast<uint16_t*>(a.qo) + t * a.qo_tok + h * a.qo_head;
+        src = static_cast<const uint16_t*>(a.q) + t * a.q_tok + (int64_t)h * a.q_head;
+        dst = static_cast<uint16_t*>(a.qo) + t * a.qo_tok + (int64_t)h * a.qo_head;
       } else {
         if (slot < 0) continue;
-        const int kv = h - (is_v ? hk : a.hq);
+        const int64_t kv = h - (is_v ? hk : a.hq);  // (a head's offset may pass 31 bits)
         src = is_v ? static_cast<const uint16_t*>(a.v) + t * a.v_tok + kv * a.v_head
                    : static_cast<const uint16_t*>(a.k) + t * a.k_tok + kv * a.k_head;
         dst = static_cast<uint16_t*>(is_v ? a.vc : a.kc) + cell + kv * a.c_head;
