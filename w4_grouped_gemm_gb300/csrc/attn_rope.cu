@@ -43,11 +43,13 @@ __device__ __forceinline__ uint64_t turn_fraction(double f) {
 }
 
 // What both kernels do first: the slots and the sines of the CTA's tokens.
-struct Tables {
+struct alignas(16) Tables {
   float2 cs[kMaxTok][kMaxPairs];  // cos, sin
   int64_t slot[kMaxTok];          // -1: nothing to append
   int64_t cell[kMaxTok];          // its offset in the cache, head 0
 };
+// (two sines and cosines are read as one float4)
+static_assert(alignof(Tables) % alignof(float4) == 0, "16-byte reads of Tables::cs");
 __device__ __forceinline__ int64_t cell_of(const RopeArgs& a, int64_t slot) {
   return (slot >> a.page_shift) * a.c_page + (slot & ((1 << a.page_shift) - 1)) * a.c_tok;
 }
