@@ -78,3 +78,17 @@ def test_rope_head_offsets_past_31_bits(oracle_lib, rot):
         # bf16's rounding, and fp32 sines of both of a pair's elements (at most 6 in size)
         assert bool(((got.double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 12 * 2.0 ** -20).all())
     assert torch.equal(vc[0, slots].cpu(), data[2])
+
+
+def test_rope_largest_number_of_tokens(oracle_lib):
+    """T = 2^31 - 1, all tokens the same row (stride 0): the call is taken, not refused for a grid
+    that wrapped."""
+    q = torch.randn(1, 1, 8, generator=torch.Generator().manual_seed(2)).to(B).cuda()
+    out = torch.zeros_like(q)
+    kc, vc = (torch.zeros(1, 16, 1, 8, dtype=B, device="cuda") for _ in range(2))
+    dims = lily.make_rope_dims(q, None, None, out, 0)
+    dims.T, dims.q_token_stride, dims.qo_token_stride = 2 ** 31 - 1, 0, 0
+    ws = lily.alloc_workspace(256)
+    lily.lily_attn_rope_append(dims, lily.PagedCache(kc, vc), q, None, None, None, None, None, out, ws)
+    torch.cuda.synchronize()
+    assert lily.lily_moe_status(ws) == 0 and torch.equal(out, q)

@@ -262,7 +262,7 @@ cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s) {
   int tok = 8 / ni;
   if (tok > a.T / (4 * 152)) tok = a.T / (4 * 152);
   tok = tok < 1 ? 1 : tok > kMaxTok ? kMaxTok : tok;
-  const dim3 grid((unsigned)((a.T + tok - 1) / tok));
+  const dim3 grid((unsigned)(((int64_t)a.T + tok - 1) / tok));  // (T may be 2^31 - 1)
   auto launch = [&](auto kern) { return launch_pdl(kern, grid, dim3(kThreads), 0, s, a, tok, lg); };
   auto by_heads = [&](auto one, auto two, auto four) {
     return ni == 1 ? launch(one) : ni == 2 ? launch(two) : launch(four);
