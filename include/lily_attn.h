@@ -174,6 +174,15 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
                             const int32_t* seq_lens, const int32_t* block_table, void* out,
                             float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Give-up limit, in nanoseconds, of every wait inside shared_prefix's kernels
+ * (for a copy or another warp of the same block): 2 s by default, counted in
+ * tries of some 4 us, at least one.  Returns the previous limit.  A block whose
+ * wait runs out sets LILY_STATUS_TIMEOUT and ends, and that call's outputs are
+ * invalid; the next call on the workspace is not affected.  For tests of the
+ * error path; 0 makes the warps that compute give up at their first wait, while
+ * copies are in flight.  Applies to calls issued after it. */
+uint64_t lily_attn_set_wait_ns(uint64_t ns);
+
 #ifdef __cplusplus
 }
 #endif

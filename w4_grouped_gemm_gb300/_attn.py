@@ -21,7 +21,7 @@ LILY_STATUS_BAD_LEN = 0x40
 
 # Every symbol include/lily_attn.h declares.
 ATTN_EXPORTS = ("lily_attn_add_rmsnorm", "lily_attn_rope_append", "lily_attn_workspace_bytes",
-                "lily_attn_shared_prefix")
+                "lily_attn_shared_prefix", "lily_attn_set_wait_ns")
 
 _DTYPES = {torch.bfloat16: _lib.LILY_DTYPE_BF16, torch.float32: _lib.LILY_DTYPE_F32,
            torch.float16: LILY_DTYPE_F16, torch.float8_e4m3fn: LILY_DTYPE_E4M3}
@@ -79,6 +79,7 @@ def _L():
             "lily_attn_rope_append": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "lily_attn_workspace_bytes": (SZ, [P, P]),
             "lily_attn_shared_prefix": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
+            "lily_attn_set_wait_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -219,3 +220,9 @@ def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, 
     rc = _L().lily_attn_shared_prefix(dims._at, cache.c._at, *p, ws.numel(), _on(stream, q))
     if rc:
         _check(rc, what)
+
+
+def lily_attn_set_wait_ns(ns: int) -> int:
+    """Give-up limit of the waits inside lily_attn_shared_prefix's kernels; returns the
+    previous limit (nanoseconds)."""
+    return int(_L().lily_attn_set_wait_ns(int(ns)))

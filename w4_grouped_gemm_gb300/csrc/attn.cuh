@@ -74,6 +74,9 @@ struct AttnArgs {
   int T, hq, hkv, G, D, page_shift, n_pages, f16;
   float scale_log2;  // softmax scale * log2(e)
   uint32_t* status;
+  // tries of a wait before it gives up (attn_set_wait): of the warps that bring
+  // keys or issue MMAs, and of those that compute
+  uint32_t wait_feed, wait_use;
 };
 
 // The shared prefix on the tensor cores of a batch with more than 64 rows per
@@ -170,16 +173,21 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
       "l"(tm), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
-// Bounded wait of a whole warp, each lane on its own barrier: at most 2^24
-// tries, each of which suspends the thread for a short time of the hardware's
-// choosing; on giving up it sets *abort and the TIMEOUT status.  The loop is a
-// handful of instructions on purpose: with a time limit in line (%globaltimer,
-// a second vote) each wait cost some 250 cycles even where it passed at once,
-// and plain polling took issue slots from the warps that compute.
+// Bounded wait of a whole warp, each lane on its own barrier: `tries` of them,
+// each of which suspends the thread until the phase is complete, for kTryNs at
+// most (measured on this GPU: 3.95 to 4.05 us, whatever suspend-time hint a try is
+// given).  On giving up it sets *abort and the TIMEOUT status; the CTA's other
+// roles, which then wait in vain too, give up by themselves.  The loop is a handful
+// of instructions on purpose: with a time limit in line (%globaltimer, a second
+// vote) each wait cost some 250 cycles even where it passed at once, plain polling
+// took issue slots from the warps that compute, and a look at *abort after a try
+// that failed took 4 percent of the tensor-core prefix (142 -> 148 us for 256
+// sequences behind 32768 keys).
+constexpr uint64_t kTryNs = 4000;
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
+                                          uint32_t tries, uint32_t* status) {
   bool ok = false;
-  for (uint32_t n = 0; n < 1u << 24 && !ok; ++n) ok = mbar_try_wait(bar, parity);
+  for (uint32_t n = 0; n < tries && !ok; ++n) ok = mbar_try_wait(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   *abort = 1;
   set_status(status, LILY_STATUS_TIMEOUT);

@@ -1,5 +1,7 @@
 // attn_api.cu -- the C ABI of include/lily_attn.h: argument checks, workspace
 // layout and the launches of each call.
+#include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 
@@ -12,6 +14,9 @@ bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 int rc_of(cudaError_t e) { return e == cudaSuccess ? LILY_OK : LILY_ERR_CUDA; }
+
+// Give-up limit of the attention kernels' waits.
+std::atomic<uint64_t> g_wait_ns{2000000000ull};
 
 constexpr int64_t kMaxStride = (int64_t)1 << 39;
 
@@ -310,6 +315,8 @@ int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache
   return rc_of(launch_rope_append(a, (cudaStream_t)stream));
 }
 
+uint64_t lily_attn_set_wait_ns(uint64_t ns) { return g_wait_ns.exchange(ns); }
+
 size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cache* cache) {
   Plan p;
   if (check_attn_dims(dims, cache) || !make_plan(*dims, *cache, p)) return 0;
@@ -354,6 +361,9 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
   a.f16 = cache->dtype == LILY_DTYPE_F16;
   a.scale_log2 = (float)((double)d.scale * 1.4426950408889634);
   a.status = static_cast<uint32_t*>(workspace);
+  const uint64_t wait = g_wait_ns.load(std::memory_order_relaxed);
+  a.wait_feed = (uint32_t)std::clamp<uint64_t>(wait / kTryNs, 1, UINT32_MAX);
+  a.wait_use = wait ? a.wait_feed : 0;
   CUtensorMap mk, mv;
   const uint32_t page = (uint32_t)cache->page_size;
   auto maps = [&](uint32_t k_rows, uint32_t v_rows) {

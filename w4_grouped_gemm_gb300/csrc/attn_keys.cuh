@@ -320,7 +320,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       }
 
       const int qb = seg % C::kQBufs;
-      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.status);
+      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.wait_feed, a.status);
       if (!ok) break;
       if (lane == 0) {
         Desc d;
@@ -364,7 +364,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
         const bool good = there && pg >= 0 && pg < a.n_pages;
         const uint32_t good_m = __ballot_sync(0xffffffffu, good);
         if (there && !good) set_status(a.status, LILY_STATUS_BAD_PAGE);
-        ok = wait_warp(empty(stage), phase ^ 1, &abort_s, a.status);
+        ok = wait_warp(empty(stage), phase ^ 1, &abort_s, a.wait_feed, a.status);
         if (!ok) break;
         if (lane == 0) {
           unsigned long long m = 0;
@@ -395,7 +395,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
     // no more units
     if (ok) {
       const int qb = seg % C::kQBufs;
-      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.status);
+      ok = wait_warp(qempty(qb), ((seg / C::kQBufs) & 1) ^ 1, &abort_s, a.wait_feed, a.status);
       if (ok && lane == 0) {
         desc[qb].part = -1;
         mbar_arrive(qfull(qb));
@@ -420,7 +420,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
     bool ok = true;
     for (int seg = 0;; ++seg) {
       const int qb = seg % C::kQBufs;
-      if (ok) ok = wait_warp(qfull(qb), (seg / C::kQBufs) & 1, &abort_s, a.status);
+      if (ok) ok = wait_warp(qfull(qb), (seg / C::kQBufs) & 1, &abort_s, a.wait_use, a.status);
       // a warp whose wait gave up takes the others with it, so that none is
       // left at a barrier
       if (!ok && lane == 0) dead_s[seg & 1] = 1;
@@ -453,7 +453,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
       for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
       for (int t = 0; t < d.tiles; ++t) {
-        ok = wait_warp(full(stage), phase, &abort_s, a.status);
+        ok = wait_warp(full(stage), phase, &abort_s, a.wait_use, a.status);
         if (!ok) break;
         if (busy) {
           const uint32_t ks_base = base + stage * C::kStageBytes;

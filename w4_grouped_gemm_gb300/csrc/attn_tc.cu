@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         const uint32_t slot = slots + mine.slot * C::kSlot;
         // (slot by slot: a warp's slots are up to a whole ring apart, and a wait
         // for a slot holds only once the filling before is known to be done)
-        if (C::kVSlots > 1) ok = wait_warp(empty(cur.slot), cur.par ^ 1, &abort_s, a.status);
-        if (!ok || !(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.status))) return;
+        if (C::kVSlots > 1) ok = wait_warp(empty(cur.slot), cur.par ^ 1, &abort_s, a.wait_feed, a.status);
+        if (!ok || !(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.wait_feed, a.status))) return;
         const bool cut = is_v && !whole;
         const uint32_t bar = cut ? land : full(mine.slot);
         if (cut ? lane == 0 : active && in_slot == 0)
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         if (cut) {
           // V of keys that are not there may hold anything, and 0 * NaN
           // would reach every row: it is set to zero before the MMAs see it
-          if (!(ok = wait_warp(land, land_par, &abort_s, a.status))) return;
+          if (!(ok = wait_warp(land, land_par, &abort_s, a.wait_feed, a.status))) return;
           land_par ^= 1;
           // (a key per lane, its pieces in an order that spreads the lanes over
           // the banks; key after key by the whole warp took 11 us of a short
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       bool ok = true;
       auto take = [&](Pos x, int n) {  // the n slots from x on have arrived
         for (int j = 0; j < n && ok; ++j, x.skip(1))
-          ok = wait_warp(full(x.slot), x.par, &abort_s, a.status);
+          ok = wait_warp(full(x.slot), x.par, &abort_s, a.wait_feed, a.status);
       };
       // Two streams issue by turns, P V of a tile and Q K of the next together:
       // their MMAs and softmaxes so stay out of step, each under the other's.
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         const int n = run.n;
         const bool shared = paired && left > 128;
         turns = C::kGroups == 2 && (paired ? shared : n > 1);
-        if (!(ok = wait_warp(q_full(g), q_par, &abort_s, a.status))) break;
+        if (!(ok = wait_warp(q_full(g), q_par, &abort_s, a.wait_feed, a.status))) break;
         q_par ^= 1;
         // the ring's order: K of the first `ahead` tiles, then V of a tile and K
         // of the tile `ahead` after it; alternating streams take every other tile
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           next_buf = !turns ? -1 : paired ? (g == 0 ? 1 : more ? 0 : -1) : t + 1 < n ? buf ^ 1 : -1;
           take(cur, C::kVSlots);
           if (more && C::kGroups == 2) take(nk, k_slots);
-          ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.status);
+          ok = ok && wait_warp(p_full(buf), p_par >> buf & 1u, &abort_s, a.wait_feed, a.status);
           p_par ^= 1u << buf;
           if (!ok) break;
           tc_fence_after();
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       const int step = !paired && C::kGroups == 2 ? 2 : 1;
       for (int t = step == 2 ? g : 0; t < run.n && !idle; t += step) {
         const int b = paired ? g : t & 1;
-        ok = wait_warp(s_full(b), s_par >> b & 1u, &abort_s, a.status);
+        ok = wait_warp(s_full(b), s_par >> b & 1u, &abort_s, a.wait_use, a.status);
         if (!ok) break;
         s_par ^= 1u << b;
         const uint4 mw = *reinterpret_cast<const uint4*>(mask_s[(run.before + t) & (kMasks - 1)]);
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           }
           if (any) {
             // O *= f, after the product that is under way
-            ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.status);
+            ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.wait_use, a.status);
             if (!ok) break;
             tc_fence_after();
             l *= f;
@@ -681,14 +681,14 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         o_par ^= 1u << o_last;
       }
       if (ok && C::kGroups == 2 && g == 1 && (idle || (!paired && run.n < 2))) {
-        ok = wait_warp(s_full(1), s_par >> 1 & 1u, &abort_s, a.status);
+        ok = wait_warp(s_full(1), s_par >> 1 & 1u, &abort_s, a.wait_use, a.status);
         s_par ^= 2u;
       }
       if (!ok) break;
 
       // the unit's partial: O / l and the log of its weight
       if (any) {
-        ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.status);
+        ok = wait_warp(o_full(o_last), (o_par >> o_last & 1u) ^ 1u, &abort_s, a.wait_use, a.status);
         if (!ok) break;
         tc_fence_after();
       }
