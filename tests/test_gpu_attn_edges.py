@@ -7,6 +7,8 @@ import torch
 
 import w4_grouped_gemm_gb300 as lily
 
+from test_gpu_attn import Batch
+
 pytestmark = pytest.mark.gpu
 B, H, F, Q = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
 
@@ -92,3 +94,40 @@ def test_rope_largest_number_of_tokens(oracle_lib):
     lily.lily_attn_rope_append(dims, lily.PagedCache(kc, vc), q, None, None, None, None, None, out, ws)
     torch.cuda.synchronize()
     assert lily.lily_moe_status(ws) == 0 and torch.equal(out, q)
+
+
+# ------------------------------------------------------------------------------------ attention: waits
+def _workspace(b):
+    """A workspace of the batch's call whose contents behind the status are no sensible number."""
+    out = torch.empty(b.q.shape, dtype=b.q.dtype, device="cuda")
+    dims = lily.make_attn_dims(b.q, out, len(b.own), b.max_q, b.prefix, b.max_own, b.table.shape[1],
+                               b.scale)
+    ws = lily.alloc_workspace(lily.lily_attn_workspace_bytes(dims, b.cache()))
+    ws[256:] = 0x7F
+    return ws
+
+
+def _give_up_then_recover(b):
+    """With a limit of 0 the warps that compute give up while copies and products are in flight: the
+    call ends with TIMEOUT.  With the limit restored the same workspace gives the right outputs."""
+    want, want_lse = b.run()
+    ws = _workspace(b)
+    prev = lily.lily_attn_set_wait_ns(0)
+    try:
+        b.run(ws=ws, status=lily.LILY_STATUS_TIMEOUT, repeat=5)
+    finally:
+        assert lily.lily_attn_set_wait_ns(prev) == 0
+    assert prev == 2_000_000_000
+    out, lse = b.run(ws=ws)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    b.check(out, lse, skip=range(2, len(b.own)))
+
+
+# prefixes on the tensor cores: one row block of two streams, pairs of row blocks (the last of one
+# block only), and heads over 128
+@pytest.mark.parametrize("D,hq,hkv,seqs,prefix,dtype", [
+    (64, 8, 1, 16, 8200, B), (128, 8, 1, 16, 8200, H), (64, 8, 1, 40, 4000, H), (128, 8, 2, 44, 4000, B),
+    (192, 1, 1, 100, 17000, H), (256, 8, 1, 40, 8000, B)])
+def test_prefix_whose_waits_run_out(oracle_lib, D, hq, hkv, seqs, prefix, dtype):
+    _give_up_then_recover(Batch(hq=hq, hkv=hkv, D=D, own=[0] * seqs, prefix=prefix, page=64, dtype=dtype,
+                                seed=D))

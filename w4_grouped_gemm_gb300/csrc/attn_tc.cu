@@ -146,10 +146,13 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
                           const __grid_constant__ CUtensorMap mv) {
   using C = Tc<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 10];
+  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 11];
   __shared__ __align__(16) uint32_t mask_s[kMasks][4];
   __shared__ uint32_t tmem_s;
   __shared__ int abort_s;
+  // 2 | parity of the last filling of a slot that copies were sent to, and of
+  // `land`: what a CTA that gives up waits for before its memory goes
+  __shared__ uint32_t armed_s[C::kSlots + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
@@ -168,7 +171,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   // buffer to itself has its scores after the product before; an alternating
   // one hands P over while the product before may still run.)
   auto o_full = [&](int i) { return bar1 + 8 * (6 + i); };
-  const uint32_t land = bar1 + 8 * 8, drain = bar1 + 8 * 9;
+  const uint32_t land = bar1 + 8 * 8;
+  auto drain = [&](int g) { return bar1 + 8 * (9 + g); };  // a stream's MMAs are done
 
   if (warp == 0) {
     if (lane == 0) {
@@ -183,7 +187,8 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         mbar_init(o_full(i), 1);
       }
       mbar_init(land, 1);
-      mbar_init(drain, C::kGroups);
+      for (int i = 0; i < 2; ++i) mbar_init(drain(i), 1);
+      for (int i = 0; i <= C::kSlots; ++i) armed_s[i] = 0;
       fence_mbar_init();
       abort_s = 0;
       prefetch_tensormap(&mk);
@@ -251,7 +256,6 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
       int land_par = 0;
       bool ok = true;
       Pos cur = {0, 0};
-      uint32_t used = 0;  // slots that this warp has filled
       auto load = [&](int h, int t) {
         const int k0 = t * kKeys, first = k0 >> ps;
         if (c_base < 0 || first < c_base || first + span > c_base + 32) {
@@ -288,9 +292,11 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
         if (!ok || !(ok = wait_warp(empty(mine.slot), mine.par ^ 1, &abort_s, a.wait_feed, a.status))) return;
         const bool cut = is_v && !whole;
         const uint32_t bar = cut ? land : full(mine.slot);
-        if (cut ? lane == 0 : active && in_slot == 0)
+        if (cut ? lane == 0 : active && in_slot == 0) {
           mbar_arrive_expect_tx(bar, __popc(cut ? good_m : good_m >> lane & slot_boxes) * box_rows * 128);
-        used |= __reduce_or_sync(0xffffffffu, 1u << mine.slot);  // (a full warp barrier too)
+          armed_s[cut ? C::kSlots : mine.slot] = 2u | (cut ? land_par : mine.par);
+        }
+        __syncwarp();
         if (good) {
           const int row = (k0 + key) & ((1 << ps) - 1);
           if (is_v) tma_load_4d(slot + at_slot, &mv, dim, row, h, pg, bar);
@@ -321,7 +327,10 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           __syncwarp();
           fence_proxy_async_smem();
           __syncwarp();
-          if (active && in_slot == 0) mbar_arrive(full(mine.slot));
+          if (active && in_slot == 0) {
+            armed_s[mine.slot] = 2u | mine.par;
+            mbar_arrive(full(mine.slot));
+          }
         }
       };
       // in the order in which the MMAs take the slots
@@ -338,12 +347,6 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           step(true, h, run.t0 + t);
           if (t + ahead < run.n) step(false, h, run.t0 + t + ahead);
         }
-      }
-      if (!ok && lane == 0) {
-        // given up: the copies in flight must land before the memory goes
-        int dead = 0;
-        for (int i = 0; i < C::kSlots; ++i)
-          if (used >> i & 1u) mbar_wait(full(i), i < cur.slot ? cur.par : cur.par ^ 1, &dead, a.status);
       }
     } else if (warp == 1 || C::kGroups == 2) {
       // ------------------------------------- MMA issuers: one warp per stream
@@ -496,14 +499,13 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           if (more) cur.skip(k_slots);
         }
       }
-      if (!ok) {
-        // given up: the MMAs in flight must be done before tensor memory goes
-        if (elect_one()) mma_commit(drain);
-        __syncwarp();
-        int dead = 0;
-        if (lane == 0) mbar_wait(drain, 0, &dead, a.status);
-        __syncwarp();
-      }
+      // The MMAs must be done before tensor memory goes: the softmax warps see to
+      // that, but not where they have given up.
+      if (elect_one()) mma_commit(drain(g));
+      __syncwarp();
+      int dead = 0;
+      if (lane == 0) mbar_wait(drain(g), 0, &dead, a.status);
+      __syncwarp();
     }
   } else {
     // --------------------------------------------------------------- softmax
@@ -730,6 +732,12 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (*static_cast<volatile int*>(&abort_s) && threadIdx.x <= C::kSlots && armed_s[threadIdx.x]) {
+    // a role has given up, nothing is sent any more: copies in flight must land
+    // before this memory goes
+    int dead = 0;
+    mbar_wait(threadIdx.x < C::kSlots ? full(threadIdx.x) : land, armed_s[threadIdx.x] & 1u, &dead, a.status);
+  }
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
