@@ -131,3 +131,13 @@ def _give_up_then_recover(b):
 def test_prefix_whose_waits_run_out(oracle_lib, D, hq, hkv, seqs, prefix, dtype):
     _give_up_then_recover(Batch(hq=hq, hkv=hkv, D=D, own=[0] * seqs, prefix=prefix, page=64, dtype=dtype,
                                 seed=D))
+
+
+# own pages and a prefix on mma.sync: 8, 16, 32 and 64 rows a unit, several units a block
+@pytest.mark.parametrize("D,hq,hkv,q_len,seqs,own,prefix,dtype", [
+    (64, 4, 2, 1, 40, 300, 0, B), (128, 8, 1, 1, 300, 60, 0, H), (256, 4, 4, 1, 5, 2000, 130, B),
+    (128, 8, 1, 2, 30, 200, 0, B), (64, 8, 1, 4, 20, 200, 700, H), (256, 8, 1, 8, 9, 150, 0, H),
+    (128, 8, 2, 5, 12, 500, 333, B)])
+def test_own_pages_whose_waits_run_out(oracle_lib, D, hq, hkv, q_len, seqs, own, prefix, dtype):
+    _give_up_then_recover(Batch(hq=hq, hkv=hkv, D=D, own=[max(q_len, own - 7 * i) for i in range(seqs)],
+                                q_lens=[q_len] * seqs, prefix=prefix, dtype=dtype, seed=D + q_len))

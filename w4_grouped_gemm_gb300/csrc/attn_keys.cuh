@@ -400,12 +400,14 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
         desc[qb].part = -1;
         mbar_arrive(qfull(qb));
       }
+      seg += ok;
     }
-    if (!ok && lane == 0) {
-      // given up: this CTA's copies must have landed before its memory goes
+    named_sync(2, kThreads);  // all roles have ended
+    if (*static_cast<volatile int*>(&abort_s) && lane == 0) {
+      // one gave up: this CTA's copies must have landed before its memory goes
       int dead = 0;
-      if (seg > 0)
-        mbar_wait(qfull((seg - 1) % C::kQBufs), ((seg - 1) / C::kQBufs) & 1, &dead, a.status);
+      for (int k = max(seg - C::kQBufs, 0); k < seg; ++k)
+        mbar_wait(qfull(k % C::kQBufs), (k / C::kQBufs) & 1, &dead, a.status);
       for (int j = 0; j < C::kStages; ++j)
         if (used >> j & 1u) mbar_wait(full(j), j < stage ? phase : phase ^ 1, &dead, a.status);
     }
@@ -732,6 +734,7 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
         }
       }
     }
+    named_sync(2, kThreads);  // (see the producer's end)
   }
 }
 
