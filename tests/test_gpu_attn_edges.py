@@ -141,3 +141,26 @@ def test_prefix_whose_waits_run_out(oracle_lib, D, hq, hkv, seqs, prefix, dtype)
 def test_own_pages_whose_waits_run_out(oracle_lib, D, hq, hkv, q_len, seqs, own, prefix, dtype):
     _give_up_then_recover(Batch(hq=hq, hkv=hkv, D=D, own=[max(q_len, own - 7 * i) for i in range(seqs)],
                                 q_lens=[q_len] * seqs, prefix=prefix, dtype=dtype, seed=D + q_len))
+
+
+def test_waits_that_run_out_leave_no_way_out_of_the_partials(oracle_lib):
+    """A block that gives up has not written where its rows' partials lie.  What stands there instead,
+    as another call's leftovers could, names the right sequence and partials far outside."""
+    for q_len, prefix in ((1, 0), (3, 500)):
+        b = Batch(hq=8, hkv=2, D=128, own=[400 - 9 * i for i in range(40)], q_lens=[q_len] * 40,
+                  prefix=prefix, seed=q_len)
+        want, want_lse = b.run()
+        ws = _workspace(b)
+        rows = sum(b.q_lens) * b.hq
+        # (the table of the rows is the workspace's last part: four words a row)
+        table = ws[-(-(-rows * 16 // 256) * 256):].view(torch.int32)[:4 * rows].view(-1, 4)
+        prev = lily.lily_attn_set_wait_ns(0)
+        try:
+            for first, number in ((1 << 30, 1 << 20), (-(1 << 30), 7), (0, 1 << 30), (1 << 30, -5)):
+                table[:, 0], table[:, 1], table[:, 2] = first, 1 << 28, number
+                table[:, 3] = torch.arange(rows, dtype=torch.int32) // (q_len * b.hq)
+                b.run(ws=ws, status=lily.LILY_STATUS_TIMEOUT)
+        finally:
+            lily.lily_attn_set_wait_ns(prev)
+        out, lse = b.run(ws=ws)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -19,7 +19,7 @@ namespace {
 // partials lie, its sequence, lse, output), so the prefix's lse are requested
 // with the first.  rows_at may hold anything for rows without own keys: an entry
 // counts where its sequence has the row's token and keys, for then this call
-// has written it.
+// has written it, and where it lies within the partials.
 template <int W>
 __global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : W == 1 ? 5 : 4)
     attn_merge_kernel(const AttnArgs a, const MergeArgs m) {
@@ -59,7 +59,10 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : W == 1 
     const int4 at = m.own.rows_at[row];
     if (at.w >= 0 && at.w < m.own.n_seqs) {
       const SeqInfo q = seq_info(m.own, a.T, at.w);
-      if (t >= q.q0 && t < q.q0 + q.qn && q.len > 0) {
+      // (a CTA that gave up may not have written it: it may be a former call's then)
+      const bool inside = at.x >= 0 && at.z >= 0 && at.z <= m.own_slots &&
+                          at.x <= m.own_slots - at.z && at.y >= 0 && at.y < m.own.rows;
+      if (t >= q.q0 && t < q.q0 + q.qn && q.len > 0 && inside) {
         w0 = at.x;
         wrow = at.y;
         nw = at.z;

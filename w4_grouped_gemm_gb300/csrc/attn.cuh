@@ -104,6 +104,7 @@ struct MergeArgs {
   // row blocks of a KV head and their rows; rows of a partial, and partials
   // of one row in it, 128 rows apart (two where streams took alternate tiles)
   int pre_tiles, pre_share, pre_blocks, pre_rows, pre_slot_rows, pre_streams;
+  int own_slots;  // partials that the own set has room for
   int own_parts;  // partials of a sequence's own keys, if all sequences were the longest
   const float* pre_o;
   const float* pre_lse;

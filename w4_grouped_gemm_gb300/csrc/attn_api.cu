@@ -429,6 +429,7 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
     o.rows_at = reinterpret_cast<int4*>(base + p.rows_at);
     o.grid = own_grid;
     m.own = o;
+    m.own_slots = (int)((int64_t)d.n_seqs * cache->n_kv_heads * o.row_blocks) + own_grid;
     m.own_parts = (int)((d.max_seq_len + kAttnTile - 1) / kAttnTile /
                         ((p.own_most + own_grid - 1) / own_grid));
   }
