@@ -22,3 +22,136 @@ def test_wait_limit_setter_returns_previous(L):
         assert lily.lily_attn_set_wait_ns(0) == 12345
     finally:
         assert lily.lily_attn_set_wait_ns(prev) == 0
+
+
+# ------------------------------------------------------------------------------------ the binding's checks
+B, H, F, Q = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+class OnGpu:
+    """A CPU tensor that says it lives on a GPU: what the binding's checks see.  A call that passes
+    them goes on to the library, which finds no device here (or is not made where there is one)."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=B):
+        self.t = torch.zeros(shape, dtype=dtype)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def _refused(f, *args):
+    with pytest.raises(lily.LilyError) as e:
+        f(*args)
+    assert e.value.code == lily.LILY_ERR_INVALID_ARG, e.value
+
+
+def _passes(f, *args):
+    """The checks let it through (the library then has no device)."""
+    if torch.cuda.is_available():
+        return
+    with pytest.raises(lily.LilyError) as e:
+        f(*args)
+    assert e.value.code in (lily.LILY_ERR_CUDA, lily.LILY_ERR_ARCH), e.value
+
+
+def _swaps(f, args, swaps):
+    """args are taken; args with any one of `swaps` (place: others in its place) are refused."""
+    _passes(f, *args)
+    for i, others in swaps.items():
+        for other in others:
+            _refused(f, *args[:i], other, *args[i + 1:])
+
+
+def test_norm_binding_checks_types(L):
+    T, d = 3, 256
+    dims = lily.make_norm_dims(T, d, B, F, H, Q, group=128)
+    x, r, w = OnGpu(T, d), OnGpu(T, d, dtype=F), OnGpu(d, dtype=H)
+    out, scales = OnGpu(T, d, dtype=Q), OnGpu(T, 2, dtype=F)
+
+    def call(*a):
+        lily.lily_attn_add_rmsnorm(dims, *a, stream=0)
+    args = (x, r, w, r, out, scales)
+    _swaps(call, args, {
+        0: [OnGpu(T, d, dtype=H), OnGpu(T, d, dtype=F), torch.zeros(T, d, dtype=B)],
+        1: [x], 2: [OnGpu(d, dtype=F)], 3: [x], 4: [x, OnGpu(T, d, dtype=torch.uint8)],
+        5: [OnGpu(T, 2), OnGpu(T, 1, dtype=F)]})
+    # dims that were filled by hand are checked alike
+    made = dims
+    dims = _attn.NormDims(T, d, 0, 1, 2, 3, 128, 1e-6, d, d, d, d)
+    _swaps(call, args, {0: [OnGpu(T, d, dtype=F)], 5: [OnGpu(T, 2)]})
+    # the number of rows may change between calls
+    dims = made
+    dims.T = T + 1
+    _refused(call, *args)
+    dims.T = T - 1
+    _passes(call, *args)
+    dims = lily.make_norm_dims(T, d, B, F, F, B)
+    _passes(call, x, None, None, None, x, None)
+
+
+def _cache(dtype=B, heads=2, D=64, pages=6, page=16):
+    return lily.PagedCache(OnGpu(pages, page, heads, D, dtype=dtype), OnGpu(pages, page, heads, D, dtype=dtype))
+
+
+def test_rope_binding_checks_types_and_sizes(L):
+    T = 5
+    i32, i64, f64 = torch.int32, torch.int64, torch.float64
+    q, k, v, qo = OnGpu(T, 4, 64), OnGpu(T, 2, 64), OnGpu(T, 2, 64), OnGpu(T, 4, 64)
+    pos, slots, freq = OnGpu(T, dtype=i32), OnGpu(T, dtype=i64), OnGpu(32, dtype=f64)
+    ws = OnGpu(256, dtype=torch.uint8)
+    dims, cache = lily.make_rope_dims(q, k, v, qo, 64), _cache()
+
+    def call(*a):
+        lily.lily_attn_rope_append(dims, cache, *a, ws, stream=0)
+    _swaps(call, (q, k, v, pos, slots, freq, qo), {
+        0: [OnGpu(T, 4, 64, dtype=H)], 1: [OnGpu(T, 2, 64, dtype=F)], 2: [OnGpu(T, 2, 64, dtype=H)],
+        3: [OnGpu(T, dtype=i64), OnGpu(T - 1, dtype=i32)], 4: [OnGpu(T, dtype=i32), OnGpu(T - 1, dtype=i64)],
+        5: [OnGpu(32, dtype=F), OnGpu(31, dtype=f64)], 6: [OnGpu(T, 4, 64, dtype=H)]})
+
+
+def test_attention_binding_checks_types_and_sizes(L):
+    T, hq, D, seqs = 6, 4, 64, 3
+    i32 = torch.int32
+    q, out, lse = OnGpu(T, hq, D), OnGpu(T, hq, D), OnGpu(T, hq, dtype=F)
+    pre, starts, lens, table = (OnGpu(n, dtype=i32) for n in (2, seqs + 1, seqs, seqs * 4))
+    cache = _cache()
+    dims = lily.make_attn_dims(q, out, seqs, 2, 20, 64, 4, 0.1)
+    ws = OnGpu(max(16, lily.lily_attn_workspace_bytes(dims, cache)), dtype=torch.uint8)
+
+    def call(*a):
+        lily.lily_attn_shared_prefix(dims, cache, *a, ws, stream=0)
+    _swaps(call, (q, pre, starts, lens, table, out, lse), {
+        0: [OnGpu(T, hq, D, dtype=H)],
+        1: [OnGpu(1, dtype=i32), OnGpu(2, dtype=torch.int64)],
+        2: [OnGpu(seqs, dtype=i32)], 3: [OnGpu(seqs - 1, dtype=i32), OnGpu(seqs, dtype=F)],
+        4: [OnGpu(seqs * 4 - 1, dtype=i32)], 5: [OnGpu(T, hq, D, dtype=F)],
+        6: [OnGpu(T, hq), OnGpu(T, hq - 1, dtype=F)]})
+    _passes(call, q, pre, None, lens, table, out, None)
+    _passes(call, 4096, 4096, 4096, 4096, 4096, 4096, 4096)     # addresses are taken as they are
+
+
+def test_dims_and_cache_have_the_same_heads(L):
+    T, ws = 5, OnGpu(1 << 20, dtype=torch.uint8)
+    x = {h: OnGpu(T, h, 64) for h in (1, 2, 4)}
+    wide = OnGpu(T, 2, 128)
+    _refused(lily.make_rope_dims, x[4], x[2], x[1], x[4], 64)     # k and v
+    _refused(lily.make_rope_dims, x[4], x[2], x[2], x[2], 64)     # q and q_out
+    _refused(lily.make_rope_dims, x[2], wide, wide, x[2], 64)     # q and k
+    _refused(lily.make_attn_dims, x[4], x[2], 5, 1, 0, 16, 1, 0.1)
+    i32, i64, f64 = torch.int32, torch.int64, torch.float64
+    pos, slots, freq = OnGpu(T, dtype=i32), OnGpu(T, dtype=i64), OnGpu(32, dtype=f64)
+    table = OnGpu(T, dtype=i32)
+    for cache, q, k, good in ((_cache(), x[4], x[2], True), (_cache(), x[4], None, True),
+                              (_cache(), None, x[2], True), (_cache(), x[4], x[1], False),
+                              (_cache(D=128), x[4], x[2], False), (_cache(D=128), x[4], None, False)):
+        dims = lily.make_rope_dims(q, k, k, q, 64)
+        args = (dims, cache, q, k, k, pos, slots if k is not None else None, freq, q, ws, 0)
+        (_passes if good else _refused)(lily.lily_attn_rope_append, *args)
+    for cache, good in ((_cache(), True), (_cache(D=128), False)):
+        dims = lily.make_attn_dims(x[4], x[4], T, 1, 0, 16, 1, 0.1)
+        (_passes if good else _refused)(lily.lily_attn_shared_prefix, dims, cache, x[4], None, None, table,
+                                        table, x[4], None, ws, 0)

@@ -2,7 +2,10 @@
 residual addition with RMSNorm, rotation and paged append, shared-prefix attention.
 
 Argument marshalling only, as in ``_lib``; the checks here are those the library cannot
-make from addresses: element types of index tensors, and that tensors live on the GPU.
+make from addresses: that tensors live on the GPU, their element types, that arrays given by a
+pointer alone (indices, lengths, scales, lse) hold as many elements as the call's dims say, and
+that the heads of the tensors that dims were made from are the cache's.  An int in a tensor's
+place is taken as an address, unchecked.
 """
 from __future__ import annotations
 
@@ -36,6 +39,7 @@ class _Struct(ctypes.Structure):
 
 
 class NormDims(_Struct):
+    types = None  # torch's, of x, residual, weight and out (make_norm_dims)
     _fields_ = ([(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "res_dtype", "w_dtype",
                                                "out_dtype", "group")]
                 + [("eps", ctypes.c_float)]
@@ -51,6 +55,7 @@ class Cache(_Struct):
 
 
 class RopeDims(_Struct):
+    hkv = D = None  # heads of k and v, and their size, where known (make_rope_dims)
     _fields_ = ([(n, ctypes.c_int32) for n in ("T", "n_q_heads", "rotary_dim", "style")]
                 + [(n, ctypes.c_int64) for n in (
                     "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride",
@@ -58,6 +63,7 @@ class RopeDims(_Struct):
 
 
 class AttnDims(_Struct):
+    D = None  # size of a head, where known (make_attn_dims)
     _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_seqs", "max_q_len",
                                                "prefix_len", "max_seq_len", "table_stride")]
                 + [("scale", ctypes.c_float)]
@@ -93,22 +99,36 @@ def _refuse(what):
     raise LilyError(LILY_ERR_INVALID_ARG, what)
 
 
-def _ptrs(what, tensors):
-    """Addresses of GPU tensors (or addresses as they are; None stays)."""
-    out = []
-    for t in tensors:
-        if t is None or t.__class__ is int:
-            out.append(t)
-        elif t.is_cuda:
-            out.append(t.data_ptr())
-        else:
-            _refuse(f"{what}: a tensor is not on the GPU")
-    return out
+def _at(what, t, dtype):
+    """Address of a GPU tensor of this type; an address as it is; None stays."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.is_cuda and t.dtype is dtype:
+        return t.data_ptr()
+    _not_taken(what, t, dtype, 0)
 
 
-def _typed(what, name, t, dtype):
-    if t is not None and t.__class__ is not int and (t.dtype is not dtype or not t.is_contiguous()):
-        _refuse(f"{what}: {name} must be a contiguous {dtype} tensor")
+def _array_at(what, t, dtype, n):
+    """The same of an array given by its pointer alone: contiguous, n elements or more."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.is_cuda and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    _not_taken(what, t, dtype, n)
+
+
+def _not_taken(what, t, dtype, n):
+    if not t.is_cuda:
+        _refuse(f"{what}: a tensor is not on the GPU")
+    if t.dtype is not dtype:
+        _refuse(f"{what}: a tensor of {t.dtype} where {dtype} belongs")
+    _refuse(f"{what}: an array must be contiguous, of {n} elements or more")
+
+
+def _alike(what, a, b):
+    """Two [tokens][heads][D] tensors (or None) have the same heads."""
+    if a is not None and b is not None and a.shape[1:] != b.shape[1:]:
+        _refuse(f"{what}: heads of {tuple(a.shape[1:])} and {tuple(b.shape[1:])}")
 
 
 def _on(stream, tensor):
@@ -135,9 +155,11 @@ class PagedCache:
         if (k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype
                 or k.stride(3) != 1):
             _refuse("cache: k and v must be 4-D, alike in shape, strides and type, last stride 1")
-        _ptrs("cache", (k, v))
+        _at("cache", k, k.dtype)
+        _at("cache", v, k.dtype)
         token, head = (1, 2) if layout == "nhd" else (2, 1)
         self.k, self.v, self.layout = k, v, layout
+        self.dtype, self.page, self.heads, self.D = k.dtype, k.shape[token], k.shape[head], k.shape[3]
 
         def stride(dim):  # a dimension of size 1 has no step; any valid one serves
             return k.stride(dim) if k.shape[dim] > 1 else max(8, (k.shape[3] + 7) // 8 * 8)
@@ -149,18 +171,34 @@ class PagedCache:
 def make_norm_dims(T, d, x_dtype, res_dtype, w_dtype, out_dtype, group=0, eps=1e-6, x_stride=None,
                    res_stride=None, res_out_stride=None, out_stride=None) -> NormDims:
     """Dims of lily_attn_add_rmsnorm; types are torch's, strides default to d."""
-    return NormDims(T, d, _code(x_dtype), _code(res_dtype), _code(w_dtype), _code(out_dtype),
+    dims = NormDims(T, d, _code(x_dtype), _code(res_dtype), _code(w_dtype), _code(out_dtype),
                     group, eps, *(d if s is None else s
                                   for s in (x_stride, res_stride, res_out_stride, out_stride)))
+    dims.types = x_dtype, res_dtype, w_dtype, out_dtype
+    return dims
+
+
+def _norm_types(d):
+    """dims.types of dims that were not made by make_norm_dims."""
+    return tuple(next((t for t, c in _DTYPES.items() if c == code), None)
+                 for code in (d.x_dtype, d.res_dtype, d.w_dtype, d.out_dtype))
 
 
 def lily_attn_add_rmsnorm(dims: NormDims, x, residual, weight, residual_out, out, scales=None,
                           stream=None):
     """residual_out = x + residual; out = its RMSNorm (see the header)."""
-    p = _ptrs("lily_attn_add_rmsnorm", (x, residual, weight, residual_out, out, scales))
-    rc = _L().lily_attn_add_rmsnorm(dims._at, *p, _on(stream, x))
+    what = "lily_attn_add_rmsnorm"
+    xt, rt, wt, ot = dims.types or _norm_types(dims)
+    n_scales = 0
+    if scales is not None:
+        group = dims.group
+        n_scales = dims.T * (dims.d // group) if group else dims.T
+    rc = _L().lily_attn_add_rmsnorm(
+        dims._at, _at(what, x, xt), _at(what, residual, rt), _at(what, weight, wt),
+        _at(what, residual_out, rt), _at(what, out, ot),
+        _array_at(what, scales, torch.float32, n_scales), _on(stream, x))
     if rc:
-        _check(rc, "lily_attn_add_rmsnorm")
+        _check(rc, what)
 
 
 def _strides(t, what):
@@ -179,20 +217,28 @@ def make_rope_dims(q, k, v, q_out, rotary_dim, style=0) -> RopeDims:
     some = q if q is not None else k
     if some is None:
         _refuse("rope dims: neither q nor k")
-    return RopeDims(some.shape[0], q.shape[1] if q is not None else 0, rotary_dim, style,
-                    *_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"),
-                    *_strides(q_out, "q_out"))
+    strides = (*_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"), *_strides(q_out, "q_out"))
+    _alike("rope dims", q, q_out)
+    _alike("rope dims", k, v)
+    if q is not None and k is not None and q.shape[2] != k.shape[2]:
+        _refuse("rope dims: heads of q and k differ in size")
+    dims = RopeDims(some.shape[0], q.shape[1] if q is not None else 0, rotary_dim, style, *strides)
+    dims.hkv, dims.D = k.shape[1] if k is not None else None, some.shape[2]
+    return dims
 
 
 def lily_attn_rope_append(dims: RopeDims, cache: PagedCache, q, k, v, positions, slots, inv_freq,
                           q_out, ws, stream=None):
     """Rotate q into q_out and k, append k and v at `slots` (see the header)."""
     what = "lily_attn_rope_append"
-    p = _ptrs(what, (q, k, v, positions, slots, inv_freq, q_out, ws))
-    _typed(what, "positions", positions, torch.int32)
-    _typed(what, "slots", slots, torch.int64)
-    _typed(what, "inv_freq", inv_freq, torch.float64)
-    rc = _L().lily_attn_rope_append(dims._at, cache.c._at, *p, ws.numel(), _on(stream, ws))
+    dt, T = cache.dtype, dims.T
+    if dims.D is not None and (dims.D != cache.D or dims.hkv not in (None, cache.heads)):
+        _refuse(f"{what}: the dims' heads are not the cache's")
+    rc = _L().lily_attn_rope_append(
+        dims._at, cache.c._at, _at(what, q, dt), _at(what, k, dt), _at(what, v, dt),
+        _array_at(what, positions, torch.int32, T), _array_at(what, slots, torch.int64, T),
+        _array_at(what, inv_freq, torch.float64, dims.rotary_dim // 2), _at(what, q_out, dt),
+        _at(what, ws, ws.dtype), ws.numel(), _on(stream, ws))
     if rc:
         _check(rc, what)
 
@@ -200,8 +246,12 @@ def lily_attn_rope_append(dims: RopeDims, cache: PagedCache, q, k, v, positions,
 def make_attn_dims(q, out, n_seqs, max_q_len, prefix_len, max_seq_len, table_stride,
                    scale) -> AttnDims:
     """Dims of lily_attn_shared_prefix for [tokens][heads][D] tensors q and out."""
-    return AttnDims(q.shape[0], q.shape[1], n_seqs, max_q_len, prefix_len, max_seq_len,
-                    table_stride, scale, *_strides(q, "q"), *_strides(out, "out"))
+    strides = (*_strides(q, "q"), *_strides(out, "out"))
+    _alike("attention dims", q, out)
+    dims = AttnDims(q.shape[0], q.shape[1], n_seqs, max_q_len, prefix_len, max_seq_len,
+                    table_stride, scale, *strides)
+    dims.D = q.shape[2]
+    return dims
 
 
 def lily_attn_workspace_bytes(dims: AttnDims, cache: PagedCache) -> int:
@@ -212,12 +262,16 @@ def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, 
                             block_table, out, lse, ws, stream=None):
     """Attention over the shared prefix and each sequence's own pages (see the header)."""
     what = "lily_attn_shared_prefix"
-    p = _ptrs(what, (q, prefix_pages, q_start, seq_lens, block_table, out, lse, ws))
-    _typed(what, "prefix_pages", prefix_pages, torch.int32)
-    _typed(what, "q_start", q_start, torch.int32)
-    _typed(what, "seq_lens", seq_lens, torch.int32)
-    _typed(what, "block_table", block_table, torch.int32)
-    rc = _L().lily_attn_shared_prefix(dims._at, cache.c._at, *p, ws.numel(), _on(stream, q))
+    dt, i32, n = cache.dtype, torch.int32, dims.n_seqs
+    if dims.D is not None and dims.D != cache.D:
+        _refuse(f"{what}: the dims' heads are not the cache's")
+    rc = _L().lily_attn_shared_prefix(
+        dims._at, cache.c._at, _at(what, q, dt),
+        _array_at(what, prefix_pages, i32, -(-dims.prefix_len // cache.page)),
+        _array_at(what, q_start, i32, n + 1), _array_at(what, seq_lens, i32, n),
+        _array_at(what, block_table, i32, n * dims.table_stride), _at(what, out, dt),
+        _array_at(what, lse, torch.float32, dims.n_tokens * dims.n_q_heads),
+        _at(what, ws, ws.dtype), ws.numel(), _on(stream, q))
     if rc:
         _check(rc, what)
 
