@@ -156,7 +156,9 @@ size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cac
  * query heads sharing KV head h being h*G .. h*G + G-1.  A row that sees
  * nothing is 0 with lse -infinity.  The prefix is read once for all sequences.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded
- * to the cache's type for the tensor cores.
+ * to the cache's type for the tensor cores (fp16: scaled by 2^7 or more, so that
+ * one 2^-21 times the largest still keeps all its bits).  Scores stay below 2^27
+ * in size: near larger ones an fp32 number is too coarse for a softmax.
  *   q             [n_tokens][n_q_heads][D], the cache's type
  *   prefix_pages  int32 [ceil(prefix_len / page_size)]; NULL when prefix_len is 0
  *   q_start       int32 [n_seqs + 1]: sequence s owns query tokens q_start[s] ..

@@ -164,3 +164,70 @@ def test_waits_that_run_out_leave_no_way_out_of_the_partials(oracle_lib):
             lily.lily_attn_set_wait_ns(prev)
         out, lse = b.run(ws=ws)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# ------------------------------------------------------------------------------------ attention: small weights
+# (tensor-core kernel or mma.sync, by the rows; one and two row blocks; heads over 128; as many heads as
+# SMs, so that a block keeps a unit's keys together)
+@pytest.mark.parametrize("D,seqs,up", [(64, 1, 14), (128, 3, 14), (256, 1, 14), (64, 65, 7), (128, 130, 7),
+                                       (192, 65, 7)])
+@pytest.mark.parametrize("floor,spread", [(26, 0), (20, 16), (26, 16)])
+@pytest.mark.parametrize("dtype", [H, B])
+def test_many_small_weights_beside_a_large_one(oracle_lib, D, seqs, up, floor, spread, dtype):
+    """One key takes nearly all of a row, 2047 others have a weight near 2^-20 or 2^-26 each: together
+    they are what the output shows, for the large one's value is 0."""
+    n, heads = 2048, 152
+    b = Batch(hq=heads, hkv=heads, D=D, own=[0] * seqs, prefix=n, page=64, dtype=dtype, seed=D)
+    gen = torch.Generator().manual_seed(floor + spread)
+    b.scale = math.log(2.0)                                    # scores are powers of two
+    b.q.zero_()
+    b.q[..., 0] = 4.0
+    below = floor + 0.25 * torch.randint(0, spread + 1, (n,), generator=gen)
+    below[0] = 0.0
+    k = torch.zeros(n, D)
+    k[:, 0] = 2.0 - below / 4                                  # exact in fp16 and bf16
+    v = (torch.randn(n, D, generator=gen) if spread else torch.ones(n, D)).to(dtype)
+    v[0] = 0.0
+    b.keys[b.prefix_cells], b.values[b.prefix_cells] = k.to(dtype)[:, None], v[:, None]
+    out, lse = b.run()
+    v = v.double()
+    p = torch.exp2(-below.double())
+    want_lse = torch.log(p.sum()) + 8.0 * math.log(2.0)
+    p /= p.sum()
+    want = p @ v
+    # roundings of the output and of the probabilities; scores' products are exact, their factor (fp32
+    # log2 e times scale) is off by 2^-24 of up to 40; exponentials and sums 2^-18; fp16 probabilities
+    # that are subnormal by 2^-25, at 2^up times their size
+    half = torch.finfo(dtype).eps / 2
+    tol = half * want.abs() + (half + 40 * 2.0 ** -23 + 2.0 ** -18) * (p @ v.abs())
+    if dtype is H:
+        tol = tol + n * 2.0 ** (-25 - up) * float(v.abs().max()) + 2.0 ** -25
+    err = (out.double() - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
+    assert bool(((lse.double() - want_lse).abs() <= 2.0 ** -20 * (1 + abs(float(want_lse)))).all())
+
+
+# (one partial per row: a prefix of one tile, or as many units as SMs, so that no unit is cut.  Where
+# partials meet, their weights are 2^lse, and an fp32 lse near 2^25 is as coarse as the scores.)
+@pytest.mark.parametrize("D,seqs,heads,n", [(64, 1, 8, 64), (128, 3, 8, 50), (256, 1, 2, 64), (64, 130, 152, 2048),
+                                            (128, 130, 152, 2048), (256, 65, 152, 2048)])
+def test_fp16_scores_near_which_numbers_are_coarse(oracle_lib, D, seqs, heads, n):
+    """Scores up to 2^25: the probabilities stay within fp16 and the output is the average of the keys
+    of the largest score."""
+    b = Batch(hq=heads, hkv=heads, D=D, own=[0] * seqs, prefix=n, page=64, dtype=H, seed=D)
+    gen = torch.Generator().manual_seed(D)
+    for q_top, k_top in ((8000.0, 4000.0), (3000.0, 700.0), (300.0, -900.0)):
+        b.q.zero_()
+        b.q[..., 0] = q_top
+        k = torch.zeros(n, D)
+        k[:, 0] = k_top - 32.0 * torch.randint(0, 4, (n,), generator=gen)
+        b.keys[b.prefix_cells] = k.to(H)[:, None]
+        b.scale = 1.0
+        out, lse = b.run()
+        v = b.values[b.prefix_cells].double()
+        best = k[:, 0] == k[:, 0].max()
+        want = v[best].mean(0)
+        # all of the best keys have the same score, whatever it was rounded to, and the next one is
+        # thousands below: roundings of P and of the output alone
+        tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -18) * v[best].abs().mean(0) + 2.0 ** -25
+        assert bool(((out.double() - want).abs() <= tol).all()), (q_top, k_top)

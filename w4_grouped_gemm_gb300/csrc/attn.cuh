@@ -200,6 +200,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The z of a softmax, 2^(c score - z), for a largest c score of zx.  fp16 loses
+// bits below 2^-14 and all below 2^-25, so with an fp16 cache the probabilities are
+// held `up` powers of two above those of a z of zx; the factor is in their sum too.
+// (A row with one dominant key over 131072 others of weight 2^-26 lost their 0.2
+// percent of the output.)  Where zx is so large that zx - up would be a coarse
+// number, z is zx: a rounding of z must not take them past fp16's range.
+constexpr float kFineZ = 1048576.f;
+template <bool F16>
+__device__ __forceinline__ float softmax_z(float zx, float up) {
+  return F16 && fabsf(zx) < kFineZ ? zx - up : zx;
+}
+
 // ---------------------------------------------------------------- 16-bit elements
 __device__ __forceinline__ float lo16_f32(uint32_t w, bool f16) {
   return f16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)))

@@ -4,7 +4,8 @@
 //
 //   out = sum_k softmax_k(scale q.k) v_k.  Over any part of the keys, with
 //   m = max s, l = sum 2^(c (s - m)), o = sum 2^(c (s - m)) v / l, c = scale log2(e),
-//   the part's weight is 2^(c m + log2 l); parts add up with those weights.
+//   the part's weight is 2^(c m + log2 l); parts add up with those weights.  (Any z
+//   near c m serves in its place; see softmax_z.)
 //
 // The shared prefix is one "sequence" whose query rows are the whole batch's,
 // so its keys and values are read once for all; each sequence's own pages are
@@ -447,8 +448,8 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
         lim_b = d.len - d.qn + 1 + (d.row0 + rb) / a.G;
       }
       const int lim_all = set.causal ? d.len - d.qn + 1 + d.row0 / a.G : d.len;  // least of the unit
-      // largest score, z = c * largest score (rounded once: every exponent and
-      // the final log use the same z), sum
+      // largest score, z = c * largest score less softmax_z's powers of two (a
+      // rounded number: every exponent and the final log use the same z), sum
       float m_a = -INFINITY, m_b = -INFINITY, z_a = 0.f, z_b = 0.f, l_a = 0.f, l_b = 0.f;
       float o[DP / 8][4];
 #pragma unroll
@@ -508,8 +509,8 @@ __device__ __forceinline__ void keys_body(const AttnArgs& a, const AttnSet& set,
           x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, 2));
           if (__any_sync(0xffffffffu, x_a != m_a || x_b != m_b)) {
             // (a row that has seen nothing keeps z = 0 and has nothing to scale)
-            const float y_a = x_a == -INFINITY ? 0.f : __fmul_rn(x_a, c);
-            const float y_b = x_b == -INFINITY ? 0.f : __fmul_rn(x_b, c);
+            const float y_a = x_a == -INFINITY ? 0.f : softmax_z<F16>(__fmul_rn(x_a, c), 14.f);
+            const float y_b = x_b == -INFINITY ? 0.f : softmax_z<F16>(__fmul_rn(x_b, c), 14.f);
             const float f_a = m_a == -INFINITY ? 0.f : ex2(z_a - y_a);
             const float f_b = m_b == -INFINITY ? 0.f : ex2(z_b - y_b);
             l_a *= f_a;

@@ -12,8 +12,9 @@
 //   O += P V       A = P from tensor memory, B = V from shared memory as it
 //                  lies (keys x dimensions: the N-major operand layout)
 // z follows the row's largest score, but O is rescaled only when it grew by
-// more than 2^8: until then P is at most 256 instead of 1, which costs no
-// precision, and the rescale (a pass over O in tensor memory) stays rare.
+// more than 2^8 (a published way of attention on this generation): until then P is
+// at most 256 times larger, which costs no precision, and the rescale (a pass over
+// O in tensor memory) stays rare.
 //
 // Warps 0 and 2 bring K and V (TMA boxes of 64 dimensions and one page) into a
 // ring of slots; warps 1 and 3 issue the MMAs of a stream each; two groups of
@@ -38,6 +39,8 @@ namespace {
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kMasks = 16;           // tiles whose key masks are kept
 constexpr int kCtrlWarps = 4;        // K, MMAs of stream 0, V, MMAs of stream 1
+constexpr float kLag = 8.f;          // powers of two by which z may be behind the largest score
+constexpr float kUp = 7.f;           // of softmax_z: kLag + kUp and a rounding stay within fp16
 
 // DP: head dimension rounded up to 64, 128 or 256.
 template <int DP>
@@ -640,11 +643,13 @@ __global__ void __launch_bounds__(Tc<DP>::kThreads, 1)
           const float zx =
               __fmul_rn(max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), fmaxf(y[6], y[7])), c);
           // (!(<=): infinities and NaN too)
-          const bool grow = have ? !(zx - z <= 8.f) : zx != -INFINITY;
+          const float most = F16 && fabsf(z) < kFineZ ? kLag + kUp : kLag;
+          const bool grow = have ? !(zx - z <= most) : zx != -INFINITY;
           if (!__any_sync(0xffffffffu, grow)) break;
-          const float f = grow && have ? ex2(z - zx) : 1.f;
+          const float z_new = softmax_z<F16>(zx, kUp);
+          const float f = grow && have ? ex2(z - z_new) : 1.f;
           if (grow) {
-            z = zx;
+            z = z_new;
             have = true;
           }
           if (any) {
