@@ -231,3 +231,18 @@ def test_fp16_scores_near_which_numbers_are_coarse(oracle_lib, D, seqs, heads, n
         # thousands below: roundings of P and of the output alone
         tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -18) * v[best].abs().mean(0) + 2.0 ** -25
         assert bool(((out.double() - want).abs() <= tol).all()), (q_top, k_top)
+
+
+# ------------------------------------------------------------------------------------ attention: bad lengths
+@pytest.mark.parametrize("seqs,prefix", [(2, 20), (2, 0), (70, 20)])
+def test_bad_lengths_where_no_sequence_may_have_keys(oracle_lib, seqs, prefix):
+    """max_seq_len 0: a length above or below it, and a range past the tokens, set BAD_LEN here too."""
+    b = Batch(own=[0] * seqs, prefix=prefix, seed=seqs)
+    for at, n in ((seqs - 1, 1), (0, -3)):
+        lens = [0] * seqs
+        lens[at] = n
+        b.check(*b.run(lens=lens, status=lily.LILY_STATUS_BAD_LEN))
+    b.check(*b.run())
+    b.q_start[seqs] = seqs + 7
+    out, lse = b.run(status=lily.LILY_STATUS_BAD_LEN)
+    b.check(out, lse, skip=[seqs - 1])

@@ -51,6 +51,9 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256, W > 8 ? 32 / W : W == 1 
   };
   pdl_wait();
   pdl_trigger();
+  if (!m.own.rows_at && blockIdx.x == 0)  // (no own keys: no key kernel has looked at the sequences)
+    for (int i = threadIdx.x; i < m.own.n_seqs; i += blockDim.x)
+      if (seq_info(m.own, a.T, i).bad) set_status(a.status, LILY_STATUS_BAD_LEN);
   const int first = part + W * lane;
   const float pre0 = first < np ? m.pre_lse[pre_row(first)] : -INFINITY;
   // partials [w0, w0 + nw) of the sequence at row wrow

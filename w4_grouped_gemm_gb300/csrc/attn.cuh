@@ -99,7 +99,7 @@ cudaError_t launch_attn_prefix_tc(const AttnArgs& a, const TcArgs& p, const CUte
                                   const CUtensorMap& mv, cudaStream_t s);
 
 struct MergeArgs {
-  AttnSet own;  // (rows_at NULL: no own keys)
+  AttnSet own;  // (rows_at NULL: no own keys, the sequences are only looked at)
   // the prefix's partials: key tiles of a unit and of a CTA (0: no prefix);
   // row blocks of a KV head and their rows; rows of a partial, and partials
   // of one row in it, 128 rows apart (two where streams took alternate tiles)

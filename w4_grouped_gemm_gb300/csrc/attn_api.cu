@@ -418,10 +418,11 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
       m.pre_streams = 1;
     }
   }
+  p.own.q_start = q_start;
+  p.own.lens = seq_lens;
+  m.own = p.own;
   if (d.max_seq_len) {
     AttnSet& o = p.own;
-    o.q_start = q_start;
-    o.lens = seq_lens;
     o.table = block_table;
     o.table_stride = d.table_stride;
     o.part_o = reinterpret_cast<float*>(base + p.own_o);
