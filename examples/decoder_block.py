@@ -93,10 +93,12 @@ class DecoderBlock:
                                    k, v, at.int(), slots, self.inv_freq, None, self.attn_ws)
 
     def slots_of(self, lens):
-        """Where the next q_len tokens of every sequence go, and their positions."""
+        """Where the next q_len tokens of every sequence go, and their positions.  A token past a
+        sequence's room goes nowhere (slot -1; its step's attention then sets BAD_LEN)."""
         at = (lens[:, None] + torch.arange(self.q_len, device=lens.device)).long()
-        pages = torch.gather(self.table.long(), 1, at // self.page)
-        return (pages * self.page + at % self.page).view(-1), (at.view(-1) + self.prefix).int()
+        pages = torch.gather(self.table.long(), 1, (at // self.page).clamp(max=self.table.shape[1] - 1))
+        slots = torch.where(at < self.own, pages * self.page + at % self.page, -1)
+        return slots.view(-1), (at.view(-1) + self.prefix).int()
 
     def step(self, residual, y):
         """residual [T][d] fp32, updated in place; y [T][d] fp32: what the block before adds to it.

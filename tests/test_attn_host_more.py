@@ -1,10 +1,16 @@
 """More of the attention side on the host (no GPU): settings, plans, and the binding's checks."""
 
+import os
+import sys
+from types import SimpleNamespace
+
 import pytest
 import torch
 
 import w4_grouped_gemm_gb300 as lily
 from w4_grouped_gemm_gb300 import _attn
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 @pytest.fixture(scope="module")
@@ -155,3 +161,23 @@ def test_dims_and_cache_have_the_same_heads(L):
         dims = lily.make_attn_dims(x[4], x[4], T, 1, 0, 16, 1, 0.1)
         (_passes if good else _refused)(lily.lily_attn_shared_prefix, dims, cache, x[4], None, None, table,
                                         table, x[4], None, ws, 0)
+
+
+# ------------------------------------------------------------------------------------ the example
+@pytest.mark.parametrize("own", [20, 32, 33])
+def test_example_tokens_past_a_sequences_room(own):
+    """Slots of a decoder block's next tokens up to, at and past the room of their sequences: the last
+    page is not passed (an index past the table would be a fault on the GPU)."""
+    from decoder_block import DecoderBlock
+    page, q_len, prefix = 16, 3, 40
+    width = -(-own // page)
+    b = SimpleNamespace(q_len=q_len, page=page, own=own, prefix=prefix,
+                        table=torch.arange(5, 5 + 2 * width, dtype=torch.int32).view(2, width))
+    for have in (0, own - 4, own - 3, own - 1, own, own + 1, own + 100):
+        lens = torch.tensor([have, 0], dtype=torch.int32)
+        slots, positions = DecoderBlock.slots_of(b, lens)
+        for j in range(q_len):
+            at = have + j
+            want = int(b.table[0, at // page]) * page + at % page if at < own else -1
+            assert int(slots[j]) == want and int(positions[j]) == prefix + at
+            assert int(slots[q_len + j]) == int(b.table[1, 0]) * page + j
