@@ -149,6 +149,14 @@ typedef struct {
 /* Device bytes of workspace (0 on bad dims). */
 size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cache* cache);
 
+/* Which kernel a call with these dims reads the shared prefix with (host only):
+ * NONE without a prefix, WARP for few rows and keys (mma.sync), TENSOR for many
+ * (tcgen05).  Negative on bad dims. */
+#define LILY_PREFIX_NONE 0
+#define LILY_PREFIX_WARP 1
+#define LILY_PREFIX_TENSOR 2
+int lily_attn_prefix_kernel(const lily_attn_dims* dims, const lily_attn_cache* cache);
+
 /* Query token j of the q_len of a sequence with seq_len own tokens (its new
  * tokens among them, appended already) sees the whole prefix and its sequence's
  * own tokens 0 .. seq_len - q_len + j.  Over those keys

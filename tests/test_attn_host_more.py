@@ -181,3 +181,23 @@ def test_example_tokens_past_a_sequences_room(own):
             want = int(b.table[0, at // page]) * page + at % page if at < own else -1
             assert int(slots[j]) == want and int(positions[j]) == prefix + at
             assert int(slots[q_len + j]) == int(b.table[1, 0]) * page + j
+
+
+# ------------------------------------------------------------------------------------ the prefix's kernel
+def test_kernel_of_the_prefix(L):
+    """Few rows or few tiles of 64 rows and keys stay on mma.sync, many go to the tensor cores (256
+    tiles, 512 for heads over 128)."""
+    def kernel(tokens, hq, hkv, prefix, D):
+        q = OnGpu(tokens, hq, D)
+        dims = lily.make_attn_dims(q, q, tokens, 1, prefix, 16, 1, 0.1)
+        return lily.lily_attn_prefix_kernel(dims, _cache(heads=hkv, D=D))
+    none, warp, tensor = lily.LILY_PREFIX_NONE, lily.LILY_PREFIX_WARP, lily.LILY_PREFIX_TENSOR
+    for D, tiles in ((64, 256), (128, 256), (136, 512), (256, 512)):
+        assert kernel(8, 8, 1, 0, D) == none
+        assert kernel(8, 8, 1, 1 << 20, D) == warp             # 64 rows
+        assert kernel(65, 1, 1, 64 * (tiles // 2 - 1), D) == warp
+        assert kernel(65, 1, 1, 64 * (tiles // 2 - 1) + 1, D) == tensor
+        assert kernel(33, 8, 4, 64 * (tiles // 8 - 1), D) == warp       # 4 heads of 66 rows
+        assert kernel(33, 8, 4, 64 * tiles // 8, D) == tensor
+    q = OnGpu(4, 4, 64)
+    _refused(lily.lily_attn_prefix_kernel, lily.make_attn_dims(q, q, 0, 1, 9, 16, 1, 0.1), _cache())

@@ -21,10 +21,11 @@ LILY_DTYPE_E4M3 = 3
 LILY_STATUS_BAD_PAGE = 0x10
 LILY_STATUS_BAD_SLOT = 0x20
 LILY_STATUS_BAD_LEN = 0x40
+LILY_PREFIX_NONE, LILY_PREFIX_WARP, LILY_PREFIX_TENSOR = 0, 1, 2
 
 # Every symbol include/lily_attn.h declares.
 ATTN_EXPORTS = ("lily_attn_add_rmsnorm", "lily_attn_rope_append", "lily_attn_workspace_bytes",
-                "lily_attn_shared_prefix", "lily_attn_set_wait_ns")
+                "lily_attn_prefix_kernel", "lily_attn_shared_prefix", "lily_attn_set_wait_ns")
 
 _DTYPES = {torch.bfloat16: _lib.LILY_DTYPE_BF16, torch.float32: _lib.LILY_DTYPE_F32,
            torch.float16: LILY_DTYPE_F16, torch.float8_e4m3fn: LILY_DTYPE_E4M3}
@@ -84,6 +85,7 @@ def _L():
             "lily_attn_add_rmsnorm": (I, [P, P, P, P, P, P, P, P]),
             "lily_attn_rope_append": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "lily_attn_workspace_bytes": (SZ, [P, P]),
+            "lily_attn_prefix_kernel": (I, [P, P]),
             "lily_attn_shared_prefix": (I, [P, P, P, P, P, P, P, P, P, P, SZ, P]),
             "lily_attn_set_wait_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
         }
@@ -256,6 +258,14 @@ def make_attn_dims(q, out, n_seqs, max_q_len, prefix_len, max_seq_len, table_str
 
 def lily_attn_workspace_bytes(dims: AttnDims, cache: PagedCache) -> int:
     return int(_L().lily_attn_workspace_bytes(dims._at, cache.c._at))
+
+
+def lily_attn_prefix_kernel(dims: AttnDims, cache: PagedCache) -> int:
+    """Which kernel reads the shared prefix: LILY_PREFIX_NONE, _WARP or _TENSOR."""
+    rc = _L().lily_attn_prefix_kernel(dims._at, cache.c._at)
+    if rc < 0:
+        _check(rc, "lily_attn_prefix_kernel")
+    return rc
 
 
 def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, q_start, seq_lens,

@@ -323,6 +323,13 @@ size_t lily_attn_workspace_bytes(const lily_attn_dims* dims, const lily_attn_cac
   return p.bytes;
 }
 
+int lily_attn_prefix_kernel(const lily_attn_dims* dims, const lily_attn_cache* cache) {
+  Plan p;
+  if (const int rc = check_attn_dims(dims, cache)) return rc;
+  if (!make_plan(*dims, *cache, p)) return LILY_ERR_UNSUPPORTED_SHAPE;
+  return !dims->prefix_len ? LILY_PREFIX_NONE : p.tc ? LILY_PREFIX_TENSOR : LILY_PREFIX_WARP;
+}
+
 int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* cache,
                             const void* q, const int32_t* prefix_pages, const int32_t* q_start,
                             const int32_t* seq_lens, const int32_t* block_table, void* out,
