@@ -1,7 +1,11 @@
 """More of the attention side on the host (no GPU): settings, plans, and the binding's checks."""
 
+import ctypes
 import os
+import random
+import subprocess
 import sys
+from pathlib import Path
 from types import SimpleNamespace
 
 import pytest
@@ -201,3 +205,59 @@ def test_kernel_of_the_prefix(L):
         assert kernel(33, 8, 4, 64 * tiles // 8, D) == tensor
     q = OnGpu(4, 4, 64)
     _refused(lily.lily_attn_prefix_kernel, lily.make_attn_dims(q, q, 0, 1, 9, 16, 1, 0.1), _cache())
+
+
+# ------------------------------------------------------------------------------------ places on the GPU
+@pytest.fixture(scope="module")
+def share(tmp_path_factory):
+    """share_grid of the library's sources, compiled for the host: (CTAs of the prefix, of the own pages)."""
+    at = tmp_path_factory.mktemp("share")
+    csrc = Path(lily.__file__).resolve().parent / "csrc"
+    (at / "s.cpp").write_text('#include "attn_share.h"\nextern "C" void share(int cap, int64_t A, int64_t B, '
+                              'int wide, int* g) { lily::share_grid(cap, A, B, wide, g[0], g[1]); }\n')
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", f"-I{csrc}", str(at / "s.cpp"), "-o",
+                    str(at / "s.so")], check=True)
+    f = ctypes.CDLL(str(at / "s.so")).share
+    f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p]
+
+    def call(cap, A, B, wide):
+        g = (ctypes.c_int * 2)()
+        f(cap, A, B, wide, g)
+        return g[0], g[1]
+    return call
+
+
+def _up(n, by):
+    return -(-n // by)
+
+
+def test_places_are_shared_for_any_length_within_the_bound(share):
+    """Whatever part b of its bound B the own pages use, the division is no slower than the two sets one
+    after the other, in tiles: w per prefix tile, and three more for the second wave of CTAs."""
+    rng = random.Random(1)
+    split = 0
+    for _ in range(20000):
+        cap, wide = rng.choice([152, 304]), rng.random() < 0.5
+        A, B = (int(2 ** rng.uniform(0, 18)) for _ in range(2))
+        w = 2 if wide else 1
+        ga, gb = share(cap, A, B, wide)
+        a0, b0 = min(A, cap), min(B, cap)
+        assert 1 <= ga <= a0 and 1 <= gb <= b0
+        if (ga, gb) == (a0, b0):
+            continue
+        split += 1
+        assert ga + gb <= cap
+        for b in {0, 1, B // 100, B // 10, B // 3, B // 2, B - 1, B}:
+            assert max(w * _up(A, ga), _up(b, gb)) <= w * _up(A, a0) + _up(b, b0) + 4, (cap, A, B, wide, b)
+    assert split > 2000
+
+
+def test_places_of_tight_and_loose_bounds(share):
+    assert share(152, 4096, 40, True) == (147, 5)              # few own keys beside a long prefix
+    assert share(304, 128, 896, True) == (128, 176)            # short runs beside a short prefix
+    ga, _ = share(152, 4096, 8192, True)                       # room for as many own tiles as the prefix's
+    assert ga >= 144
+    ga, _ = share(304, 128, 65536, True)
+    assert ga >= 64
+    assert share(304, 0, 500, True) == (0, 304) and share(304, 500, 0, False) == (304, 0)
+    assert share(304, 100, 200, True) == (100, 200)

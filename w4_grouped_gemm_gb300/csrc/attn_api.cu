@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "attn.cuh"
+#include "attn_share.h"
 
 namespace lily {
 namespace {
@@ -160,29 +161,6 @@ bool make_plan(const lily_attn_dims& d, const lily_attn_cache& c, Plan& p) {
   }
   p.bytes = off;
   return true;
-}
-
-// CTAs for the prefix's A tiles and the own pages' B tiles (at most; half of it
-// is taken) in one launch on a GPU that holds `cap`.  Either both sets take all
-// it holds, one after the other, or they share it so that both take about as
-// long; a prefix tile of more rows than an own one (wide) counts twice, and a
-// CTA costs about three tiles besides its own.  (4 sequences of 257 own keys
-// behind 131072, D = 256: 63.9 us with the own pages' 40 CTAs after the prefix's
-// 152, 58.0 with 5 beside its 147.)
-void share_grid(int cap, int64_t A, int64_t B, bool wide, int& ga, int& gb) {
-  ga = (int)(A < cap ? A : cap);
-  gb = (int)(B < cap ? B : cap);
-  if (ga + gb <= cap || cap < 2) return;
-  auto per = [](int64_t n, int64_t g) { return (n + g - 1) / g; };
-  const int64_t half = (B + 1) / 2, w = wide ? 2 : 1;
-  int64_t both = per(w * A + half, cap);  // the time that each set takes
-  if (both < w) both = w;
-  while (per(A, both / w) + per(half, both) > cap) both += 1 + both / 64;
-  if (both + 3 <= w * per(A, ga) + per(half, gb) + 6) {
-    const int64_t left = cap - per(half, both);
-    ga = (int)per(A, per(A, A < left ? A : left));  // the least that take as long
-    gb = (int)(B < cap - ga ? B : cap - ga);
-  }
 }
 
 // The cache as a 4-D tensor [page][head][token][D]; boxes of 64 dimensions
