@@ -8,6 +8,7 @@ import torch
 import w4_grouped_gemm_gb300 as lily
 
 from test_gpu_attn import Batch
+from test_gpu_attn_norm_rope import _check_norm
 
 pytestmark = pytest.mark.gpu
 B, H, F, Q = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
@@ -39,6 +40,17 @@ def test_norm_maximum_whose_scale_rounds_to_zero(oracle_lib, d, group, x_pad, ou
     assert bool((codes[1::2, 1:] == 448).all()) and bool((codes[1::2, 0] == 0).all())
     # (rows of ones: n = 1 to a few roundings of fp32)
     assert bool(((scales[1::2].double() * 448 - 1).abs() <= 2.0 ** -20).all())
+
+
+# widths that fill eight warps, nearly, and not quite, with one, two and four chunks a thread
+@pytest.mark.parametrize("d", [1536, 1656, 1664, 1984, 2048, 2056, 3320, 3328, 3968, 4096, 6592, 6656, 7936, 8192, 8200])
+@pytest.mark.parametrize("xt,rt,ot", [(B, F, Q), (F, F, Q), (H, H, Q), (B, B, B), (F, B, H)])
+def test_norm_widths_about_eight_warps(oracle_lib, d, xt, rt, ot):
+    _check_norm(9, d, xt, rt, F, ot, 0, seed=d)
+    if ot is Q and d % 64 == 0:
+        _check_norm(9, d, xt, rt, F, ot, 64, seed=d)
+    if ot is Q and d % 128 == 0:
+        _check_norm(9, d, xt, rt, F, ot, 128, seed=d)
 
 
 # ------------------------------------------------------------------------------------ rope, append

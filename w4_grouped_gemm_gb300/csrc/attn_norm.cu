@@ -13,6 +13,7 @@
 // row of 2048 2.1 us in a graph.
 #include <climits>
 #include <cuda_fp8.h>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -132,8 +133,6 @@ __device__ __forceinline__ void scale8(float (&r)[8], const float (&w)[16], floa
 enum Lay { kAny, kWhole, kShift };
 
 // A row on WPR warps, or on a block of as many warps as its chunks need (0).
-// (Eight warps known when compiling take 82 us for 16384 rows of 4096 in bf16,
-// out in 8 bits; as a block of any size 90.)
 // XT, RT, OT: element types known when compiling, -1: asked at run time (OT 0:
 // one of the 16-bit types).  Asked at run time they cost half of the issue
 // slots, which then bound the kernel (16384 rows of 4096 into 8 bits: 93 us).
@@ -426,13 +425,19 @@ cudaError_t launch_types(const NormArgs& a, Lay lay, int chunks, cudaStream_t s)
 template <int WPR, int C>
 cudaError_t launch_as(const NormArgs& a, Lay lay, int n8, cudaStream_t s) {
   constexpr int B = LILY_DTYPE_BF16, H = LILY_DTYPE_F16, F = LILY_DTYPE_F32, Q = LILY_DTYPE_E4M3;
-  const bool q = a.ot == Q;
+  constexpr bool kOnly8 = WPR == 8 && C == 4;  // (16-bit rows do not come here)
+  auto types = [&](auto x, auto r) {
+    constexpr int X = decltype(x)::value, R = decltype(r)::value;
+    return a.ot == Q ? launch_types<WPR, C, X, R, Q>(a, lay, n8, s)
+                     : launch_types<WPR, C, X, R, kOnly8 ? Q : 0>(a, lay, n8, s);
+  };
+  using Bf = std::integral_constant<int, B>;
+  using Hf = std::integral_constant<int, H>;
+  using Ff = std::integral_constant<int, F>;
   if (lay != kAny && (a.rt == F || a.rt == a.xt)) {
-    if (a.xt == B && a.rt == B) return q ? launch_types<WPR, C, B, B, Q>(a, lay, n8, s) : launch_types<WPR, C, B, B, 0>(a, lay, n8, s);
-    if (a.xt == B) return q ? launch_types<WPR, C, B, F, Q>(a, lay, n8, s) : launch_types<WPR, C, B, F, 0>(a, lay, n8, s);
-    if (a.xt == H && a.rt == H) return q ? launch_types<WPR, C, H, H, Q>(a, lay, n8, s) : launch_types<WPR, C, H, H, 0>(a, lay, n8, s);
-    if (a.xt == H) return q ? launch_types<WPR, C, H, F, Q>(a, lay, n8, s) : launch_types<WPR, C, H, F, 0>(a, lay, n8, s);
-    return q ? launch_types<WPR, C, F, F, Q>(a, lay, n8, s) : launch_types<WPR, C, F, F, 0>(a, lay, n8, s);
+    if (a.xt == B) return a.rt == B ? types(Bf(), Bf()) : types(Bf(), Ff());
+    if (a.xt == H) return a.rt == H ? types(Hf(), Hf()) : types(Hf(), Ff());
+    return types(Ff(), Ff());
   }
   return launch_types<WPR, C, -1, -1, -1>(a, lay, n8, s);
 }
@@ -458,12 +463,22 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
     lay = kShift;
     n8 = (a.d + 14) / 8;
   }
+  // Rows that fill 13/16 of eight warps with C chunks a thread take eight warps known
+  // when compiling, others a block of as many as they need.  Measured, a block of
+  // any size against eight warps, 2^26 bf16 elements into 8 bits with groups of 128,
+  // us: widths 1536 107 / 106, 1664 121 / 104, 1792 114 / 97, 2048 108 / 91;
+  // 2816 89 / 91, 3328 90 / 84, 4096 84 / 77; 6144 86 / 82, 7168 91 / 80, 8192 89 /
+  // 76; less filled ones lose (1152 119 / 129, 2304 88 / 103, 4608 86 / 95).  Into 16
+  // bits, which HBM bounds, both take the same (2048 80 / 78, 4096 78 / 78) but with
+  // four chunks eight warps are slower (8192, fp32 residual 117 / 119).
+  auto fills = [&](int C) { return lay == kWhole && n8 <= 256 * C && 16 * n8 >= 13 * 256 * C; };
   prof_begin(K_ATTN_NORM, s);
   cudaError_t e;
   if (n8 <= 32) e = launch_as<1, 1>(a, lay, n8, s);
   else if (n8 <= 128) e = launch_as<4, 1>(a, lay, n8, s);
-  else if (lay == kWhole && n8 > 224 && n8 <= 256) e = launch_as<8, 1>(a, lay, n8, s);
-  else if (lay == kWhole && n8 > 448 && n8 <= 512) e = launch_as<8, 2>(a, lay, n8, s);
+  else if (fills(1)) e = launch_as<8, 1>(a, lay, n8, s);
+  else if (fills(2)) e = launch_as<8, 2>(a, lay, n8, s);
+  else if (fills(4) && a.ot == LILY_DTYPE_E4M3) e = launch_as<8, 4>(a, lay, n8, s);
   // (kShift holds the weights of a chunk twice: one chunk per thread where that does)
   else if (n8 <= (lay == kShift ? 512 : 256)) e = launch_as<0, 1>(a, lay, n8, s);
   else if (n8 <= 1024) e = launch_as<0, 2>(a, lay, n8, s);
