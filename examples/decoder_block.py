@@ -2,7 +2,9 @@
 share a prefix, from the residual stream through attention and the MoE expert layer back to it.
 
     residual += y                              lily_attn_add_rmsnorm (8-bit rows with scales)
-    q, k, v = rows @ w_qkv                     the caller's projection, here a plain product
+    q, k, v = rows @ w_qkv                     the caller's projection, here a plain product of
+                                               the rows taken back to bf16; an 8-bit one would
+                                               take codes and scales as they are
     rotate q and k, append k and v             lily_attn_rope_append
     attention                                  lily_attn_shared_prefix
     residual += heads @ w_o                    lily_attn_add_rmsnorm (bf16 rows)

@@ -62,14 +62,20 @@ typedef struct {
 /* r = residual + x (fp32), n = r / sqrt(mean(r^2) + eps) * weight, and
  *   residual_out = r rounded to res_dtype,
  *   out = n rounded to BF16 / F16; or, E4M3, out = n / s rounded with
- *   s = max|n| / 448 over each group of columns (0 where that is 0, and out is 0).
- * The norm is taken of the fp32 sum, before the residual's rounding.
+ *   s = max|n| / 448 over each group of columns (0 where that is 0 or rounds to
+ *   0, and out is 0).
+ * The norm is taken of the fp32 sum, before the residual's rounding.  The 8-bit
+ * code is that of n times 448 / max|n|, a reciprocal rounded to fp32, or of n / s
+ * in rows read element by element: next to a border between two codes either may
+ * come out, and rows of another alignment may differ in such a code.
  *   residual      NULL: r = x
  *   weight        [d], or NULL: ones
  *   residual_out  may be residual itself (in place), or NULL: not stored
  *   scales        fp32 [T][d / group] ([T] when group is 0): E4M3 only, else NULL
- * Rows whose base or stride is not a multiple of eight elements are read and
- * written element by element.  A row with a NaN or an infinity gives NaN there
+ * Rows that all lie on multiples of eight elements are read and written in
+ * vectors, and so are, without groups, rows of odd widths whose operands have the
+ * same distance from one (as contiguous tensors do); others element by element.
+ * A row with a NaN or an infinity gives NaN there
  * (E4M3: its scale too). */
 int lily_attn_add_rmsnorm(const lily_attn_norm_dims* dims, const void* x, const void* residual,
                           const void* weight, void* residual_out, void* out, float* scales,
@@ -111,8 +117,10 @@ typedef struct {
 
 /* The pair (a, b) number i of token t turns by the angle positions[t] *
  * inv_freq[i]: (a cos - b sin, b cos + a sin), in fp32, rounded once.  The
- * angle is exact to 2^-50 of a turn at any position of 31 bits (it is a 64-bit
- * fraction of a turn, not an fp32 product).
+ * frequency is taken as a 64-bit fraction of a turn, cut off, and the product with
+ * the position keeps its last 64 bits: the angle is off by less than position *
+ * 2^-64 of a turn (2^-33 at 31 bits), which its rounding to fp32 for the sines
+ * (2^-26 of a turn) hides.
  *   positions   int32 [T]
  *   inv_freq    fp64 [rotary_dim / 2], radians per position
  *   slots       int64 [T]: token t goes to page slots[t] / page_size, row
@@ -135,7 +143,9 @@ int lily_attn_rope_append(const lily_attn_rope_dims* dims, const lily_attn_cache
  * max_q_len    at least every sequence's number of query tokens; 1 in decode
  * prefix_len   tokens of the shared prefix, 0 for none
  * max_seq_len  at least every sequence's own length; table_stride * page_size
- *              or less
+ *              or less.  The launch is planned by this bound, not by the
+ *              lengths, which only the device knows: the room of the sequences
+ *              serves in a captured graph, a tight bound is up to a sixth faster
  * table_stride entries of block_table per sequence
  * scale        softmax scale, > 0
  * strides      elements, per token and per head, of q and out: multiples of 8
@@ -178,7 +188,8 @@ int lily_attn_prefix_kernel(const lily_attn_dims* dims, const lily_attn_cache* c
  *   lse           fp32 [n_tokens][n_q_heads] or NULL
  * A page index outside the cache sets LILY_STATUS_BAD_PAGE and its keys are
  * skipped; a length or range outside its bounds sets LILY_STATUS_BAD_LEN and is
- * clamped.  Outputs are the same bits on every run with the same arguments. */
+ * clamped (a token that two clamped ranges share sees either's keys).  Outputs are
+ * otherwise the same bits on every run with the same arguments. */
 int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* cache,
                             const void* q, const int32_t* prefix_pages, const int32_t* q_start,
                             const int32_t* seq_lens, const int32_t* block_table, void* out,

@@ -74,7 +74,7 @@ int check_attn_dims(const lily_attn_dims* d, const lily_attn_cache* c) {
 // Rows per unit: 8, 16, 32 or 64, the least that holds `rows` (64 at most).
 int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
-// The prefix goes to the tensor-core kernel where it has more rows per KV head
+// The prefix goes to the tensor-core kernel (LILY_PREFIX_TENSOR) where it has more rows per KV head
 // than one mma.sync row block (above, both read it once) and enough tiles of 64
 // rows and keys for that kernel's launch, its load of Q and its larger partials
 // to pay (128 sequences of 8 rows on one KV head, D = 128: 15.9 against 17.3 us

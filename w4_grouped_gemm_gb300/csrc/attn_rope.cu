@@ -6,7 +6,9 @@
 // At far positions an fp32 product loses the angle (position 10^6 leaves an
 // error of 0.06 rad), and fp64 arithmetic is slow on this GPU.  So frequencies
 // become 64-bit fractions of a turn; position times fraction is then one 64-bit
-// integer multiply whose overflow is exactly the whole turns that do not matter.
+// integer multiply whose overflow is exactly the whole turns that do not matter;
+// what the fraction was cut off by (below 2^-64) grows with the position to 2^-33 of
+// a turn at most.
 //
 // HBM bounds it: q, k and v are read once, in 16-byte pieces, and written
 // once.  A CTA takes whole tokens, so that a token's sines are computed once

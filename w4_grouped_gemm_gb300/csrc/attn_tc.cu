@@ -8,7 +8,9 @@
 // 128-key tiles:
 //   S = Q K^T      A = Q, B = K from shared memory, S in tensor memory
 //   P = 2^(c S - z) one thread per row: 128 scores in registers, no shuffles;
-//                  P overwrites S in tensor memory (16 bits)
+//                  P overwrites S in tensor memory, rounded to the cache's 16
+//                  bits, which the MMA takes (a wider type has half its rate);
+//                  its sum is of the unrounded ones
 //   O += P V       A = P from tensor memory, B = V from shared memory as it
 //                  lies (keys x dimensions: the N-major operand layout)
 // z follows the row's largest score, but O is rescaled only when it grew by
@@ -27,7 +29,7 @@
 // alternates between them.
 //
 // Measured: 256 sequences of 8 rows on each of 4 KV heads behind 32768 keys,
-// D = 128 (137 GFLOP): 141 us with the own pages and the merge, 0.97 PFLOP/s.  A
+// D = 128 (137 GFLOP): 139 us with the own pages and the merge, 0.99 PFLOP/s.  A
 // tile of 256 rows takes some 3000 cycles, 2200 of which the MMAs need; the rest
 // is the chain from a score to its probability (wait, load, exponentials, store,
 // arrive), which two streams cover in part.
