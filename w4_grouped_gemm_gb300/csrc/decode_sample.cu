@@ -181,7 +181,7 @@ struct Shared {
   uint32_t cta_max[kMaxCluster], cta_min[kMaxCluster], cta_least[kMaxCluster];
   uint32_t warp_max[kWarps], warp_min[kWarps], warp_least[kWarps];
   uint16_t shorts[kWarps][kShort];            // each warp's slots with a logit in a range
-  uint32_t n_list[2];  // (a row gathers twice at most)
+  uint32_t n_list[3];  // of each gather: the search by count's, the search by mass's, the last one's
   uint64_t cut_floor, cut_mass;
   uint32_t bin, found, bin_cnt, cnt_before;
   uint64_t mass_before, mass;
@@ -354,7 +354,8 @@ __device__ __forceinline__ void for_some(const Shared& s, const Row& r, int n, F
 }
 
 // The cluster's tokens for which f(logit, token) is true, kFew at most, into the list
-// of its first CTA, in any order; ends with a barrier of the cluster.
+// of its first CTA, in any order, counted from 0 by n_list[which]; ends with a barrier of
+// the cluster.
 template <typename F>
 __device__ __forceinline__ void gather(Shared& s, const Row& r, int which, int listed, F f) {
   for_some(s, r, listed, [&](float x, int token) {
@@ -483,14 +484,15 @@ __device__ Found search(Shared& s, const Row& r, const Mass& weigh, float m, boo
     if (bin_cnt <= kFew) {
       // the first CTA puts the bin's in order and says from which number on the run goes
       if (!tried) list();
-      gather(s, r, 0, run.listed, [&](float x, int token) {
+      const int which = by_mass ? 1 : 0;  // (both searches of a row may come here)
+      gather(s, r, which, run.listed, [&](float x, int token) {
         const uint64_t o = order_of(x, token);
         return o >= lo && o <= hi && (run.last < 0 || run.step(m, x) == run.last) && (!by_mass || weigh(x));
       });
       if (r.rank == 0) {
         uint64_t o, w = 0, all_w;
         uint32_t place;
-        const bool in = in_order(s, 0, o, place);
+        const bool in = in_order(s, which, o, place);
         if (in) w = weigh(of_key((uint32_t)(o >> kIndexBits)));
         if (b < kFew) s.weight[b] = 0;
         __syncthreads();
@@ -526,10 +528,10 @@ __device__ Found search(Shared& s, const Row& r, const Mass& weigh, float m, boo
 // held; 0: p times that of the k), min-p and the draw.
 __device__ void finish(Shared& s, const Mass& weigh, float m, uint32_t k, float p, uint64_t target, uint64_t least_mass,
                        float u, float temperature, int32_t* token_out, float* logprob_out) {
-  const uint32_t n = min(s.n_list[1], (uint32_t)kFew), i = threadIdx.x;
+  const uint32_t n = min(s.n_list[2], (uint32_t)kFew), i = threadIdx.x;
   uint64_t o;
   uint32_t place;
-  const bool in = in_order(s, 1, o, place) && place < k;
+  const bool in = in_order(s, 2, o, place) && place < k;
   const float x = of_key((uint32_t)(o >> kIndexBits));
   const uint32_t token = kIndexMask - ((uint32_t)o & kIndexMask);
   const uint64_t w = in ? weigh(x) : 0;
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (nan) set_status(a.status, LILY_STATUS_NAN_LOGIT);
 
   // ---- the largest and the least logit, and the floor
-  if (threadIdx.x < 2) s.n_list[threadIdx.x] = 0;
+  if (threadIdx.x < 3) s.n_list[threadIdx.x] = 0;
   {
     const uint32_t key = key_of(most);
     const uint32_t top = __reduce_max_sync(0xffffffffu, key), low = __reduce_min_sync(0xffffffffu, key_of(fewest));
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // (by mass the list is that of the last steps alone)
     const int listed = run.last < 0 ? run.listed : -1;
     const float x_floor = of_key((uint32_t)(run.floor >> kIndexBits));
-    gather(s, r, 1, listed, [&](float x, int token) {
+    gather(s, r, 2, listed, [&](float x, int token) {
       return !(x < x_floor) && order_of(x, token) >= run.floor && (run.last < 0 || run.step(m, x) <= run.last) && weigh(x);
     });
     if (r.rank == 0)
