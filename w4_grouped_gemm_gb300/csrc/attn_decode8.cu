@@ -31,8 +31,10 @@
 // it by 4: most steps then need neither the maximum nor a rescaling, and a vote tells.
 // fp16 for the probabilities: 2^(z - m) v_scale, at most 2^4 times the largest v_scale,
 // is held 2^(10 - e) times as large, e the exponent of the largest v_scale so far, so
-// that it ends below 2^15 and all bits are kept from 2^-24 of the reference on.  q is
-// brought to fp16's range by a power of two for each row.
+// that it ends below 2^15 and all bits are kept from 2^-24 of the reference on.  e may be
+// that of any fp32 number: powers of two by it are taken in two factors where one would
+// leave fp32's range, and partial outputs are divided by their sums.  q is brought to
+// fp16's range by a power of two for each row.
 //
 // Measured: 4 sequences of up to 131072 keys, 2 KV heads of 256, 86 us, 5.8 TB/s; 128 of
 // up to 4096, 97 us, 6.0 TB/s; one of 301 keys 8.2 us, half of it the look-ups before
@@ -149,6 +151,12 @@ __device__ __forceinline__ void row_at(const Decode8Args& a, const Cursor& c, in
 __device__ __forceinline__ int first_tile(int total, int grid, int i) {
   const uint32_t each = (uint32_t)total / grid, rest = total - each * grid;
   return (int)(each * i + rest * i / grid);
+}
+
+// 2^e in two factors, for e of -252 to 254.
+__device__ __forceinline__ float2 power2(int e) {
+  const int half = e >> 1;
+  return make_float2(__uint_as_float((uint32_t)(127 + half) << 23), __uint_as_float((uint32_t)(127 + e - half) << 23));
 }
 
 // Tries of the wait for the last copies: 2 s.
@@ -417,8 +425,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     for (int n = 0; n < kMT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
-    int ev = -100;  // exponent of the largest v_scale so far
-    float fv = __uint_as_float((uint32_t)(127 + 10 + 100) << 23);  // 2^(10 - ev)
+    int ev = -127;                 // exponent of the largest v_scale so far
+    float2 fv = power2(10 - ev);   // 2^(10 - ev)
+    float next_v = 1.17549435e-38f;  // 2^(ev + 1): a scale of that size moves ev
 
     const int n_tiles = min(left, out.tiles - out.tile);
 #pragma unroll 1
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           vs[b][i] = __uint_as_float(lds32(side + C::kTile * 4 + (16 * b + key_of_lane + 8 * i) * 4));
-          ahead |= (plain || (there >> b & 1)) && fabsf(vs[b][i]) * fv >= 2048.f;
+          ahead |= (plain || (there >> b & 1)) && fabsf(vs[b][i]) >= next_v;
         }
       }
       if (__any_sync(0xffffffffu, ahead)) {
@@ -491,10 +500,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         const int key = lane % C::kKeys;
         uint32_t vmax = lds32(side + C::kTile * 4 + key * 4) & 0x7FFFFFFFu;
         vmax = __reduce_max_sync(0xffffffffu, (there >> (key >> 4) & 1) && vmax < 0x7F800000u ? vmax : 0u);
-        const int e_new = max(ev, min(max((int)(vmax >> 23) - 127, -100), 120));
-        fv = __uint_as_float((uint32_t)(127 + 10 - e_new) << 23);
-        const float down = __uint_as_float((uint32_t)max(127 - (e_new - ev), 1) << 23);
+        const int e_new = max(ev, (int)(vmax >> 23) - 127);
+        const float down = __uint_as_float((uint32_t)max(127 - (e_new - ev), 0) << 23);
         ev = e_new;
+        fv = power2(10 - ev);
+        next_v = __uint_as_float((uint32_t)(ev + 128) << 23);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float top = m[i];
@@ -515,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 #pragma unroll
       for (int b = 0; b < C::kBlocks; ++b) {
         if (!plain && !(there >> b & 1)) continue;  // (what lies there is another tile's)
-        vs[b][0] *= fv;
-        vs[b][1] *= fv;
+        vs[b][0] = vs[b][0] * fv.x * fv.y;
+        vs[b][1] = vs[b][1] * fv.x * fv.y;
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -578,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-      if (g == 0) stat[odd][warp][2 * t + i] = make_float4(m[i], l[i], __uint_as_float((uint32_t)(127 - 10 + ev) << 23), 0.f);
+      if (g == 0) stat[odd][warp][2 * t + i] = make_float4(m[i], l[i], __int_as_float(ev), 0.f);
     }
     auto join = [&](int w, int n) {
       constexpr int kPer = C::kKeys * C::kWide / 512, kAcross = DP / C::kWide;  // tiles of 512 bytes; halves of a row
@@ -591,6 +601,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     for (int n = 0; n < kMT; ++n) *join(warp, n) = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
     named_sync(1, kUsers);
     float to[2], sum[2], by_warp[kWarps][2];
+    int e_all = -127;  // the largest of the warps' exponents, which the outputs' sum is held by
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) e_all = max(e_all, __float_as_int(stat[odd][k][0].z));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float4 w[kWarps];
@@ -606,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         // (a maximum of -infinity with a sum: a NaN)
         const float f = w[k].x == -INFINITY ? (w[k].y == 0.f ? 0.f : 1.f) : ex2(w[k].x - to[i]);
         sum[i] += w[k].y * f;
-        by_warp[k][i] = w[k].x == -INFINITY ? (w[k].y == 0.f ? 0.f : w[k].y) : f * w[k].z;
+        const float down = __uint_as_float((uint32_t)max(127 - (e_all - __float_as_int(w[k].z)), 0) << 23);
+        by_warp[k][i] = w[k].x == -INFINITY ? (w[k].y == 0.f ? 0.f : w[k].y) : f * down;
       }
     }
     odd ^= 1;
@@ -614,13 +628,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     const bool done = whole && ends;
     const int part = 2 * blockIdx.x + (whole ? 1 : 0);
     uint16_t* dst[2];  // of rows 2t and 2t + 1
+    const float2 held = power2(e_all - 10);
     float by[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       int j, head;
       row_at(a, out, 2 * t + i, j, head);
       dst[i] = static_cast<uint16_t*>(a.out) + (int64_t)(out.q0 + j) * a.out_tok + (int64_t)head * a.out_head;
-      by[i] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+      by[i] = sum[i] == 0.f ? 0.f : held.x / sum[i];
     }
 #pragma unroll
     for (int n = warp; n < kMT; n += kWarps) {
@@ -630,13 +645,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         const float4 x = *join(w, n);
         v.x += x.x * by_warp[w][0], v.y += x.y * by_warp[w][1], v.z += x.z * by_warp[w][0], v.w += x.w * by_warp[w][1];
       }
+      v.x = v.x * by[0] * held.y, v.y = v.y * by[1] * held.y, v.z = v.z * by[0] * held.y, v.w = v.w * by[1] * held.y;
       // dimensions d and d + 1 of both rows
       const int d = DP == 64 ? 8 * g + 2 * n : 128 * (n >> 3) + 16 * g + 2 * (n & 7);
       if (!done) {
         a.part_o[((size_t)part * kMT + n) * 32 + lane] = v;
       } else if (d < a.D) {
-        if (2 * t < rows) *reinterpret_cast<uint32_t*>(dst[0] + d) = pack16(v.x * by[0], v.z * by[0], a.f16);
-        if (2 * t + 1 < rows) *reinterpret_cast<uint32_t*>(dst[1] + d) = pack16(v.y * by[1], v.w * by[1], a.f16);
+        if (2 * t < rows) *reinterpret_cast<uint32_t*>(dst[0] + d) = pack16(v.x, v.z, a.f16);
+        if (2 * t + 1 < rows) *reinterpret_cast<uint32_t*>(dst[1] + d) = pack16(v.y, v.w, a.f16);
       }
     }
     if (warp == 0 && g == 0) {
@@ -714,10 +730,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode8_merge_kernel(const D
   float sum = 0.f;
   for (int p = threadIdx.x / kRows; p < parts; p += kAcross) {
     const float2 ml = a.part_ml[part_of(p) * kRows + row];
-    // (a maximum of -infinity with a sum: a NaN)
-    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - to);
+    // (a maximum of -infinity with a sum: a NaN, and so is the weight)
+    const float w = ml.x == -INFINITY ? ml.y : ex2(ml.x - to) * ml.y;
     weight[p * kRows + row] = w;
-    sum += w * ml.y;
+    sum += w;
   }
 #pragma unroll
   for (int o = kRows; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -726,8 +742,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode8_merge_kernel(const D
   const int n = blockIdx.y, g = lane >> 2, t = lane & 3;
   const float* w0 = weight + 2 * t;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  // (shares of rows 2t and 2t + 1: a sum of values near fp32's largest would not fit it)
+  float total[2] = {0.f, 0.f}, by[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) total[i] += part_sum[w][2 * t + i];
+    by[i] = total[i] == 0.f ? 0.f : 1.f / total[i];
+  }
   auto add = [&](const float4& y, int p) {
-    const float2 w = *reinterpret_cast<const float2*>(w0 + p * kRows);
+    float2 w = *reinterpret_cast<const float2*>(w0 + p * kRows);
+    w.x *= by[0], w.y *= by[1];
     v.x += w.x * y.x, v.y += w.y * y.y, v.z += w.x * y.z, v.w += w.y * y.w;
   };
 #pragma unroll
@@ -749,16 +774,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode8_merge_kernel(const D
   for (int i = 0; i < 2; ++i) {
     const int at = 2 * t + i;
     if (at >= rows) continue;
-    float total = 0.f, top = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) total += part_sum[w][at], top = fmaxf(top, part_max[w][at]);
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, part_max[w][at]);
     const int rr = rb * kRows + at, j = rr / a.G, head = h * a.G + rr - j * a.G;
-    const float by = total == 0.f ? 0.f : 1.f / total;
     uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(q0 + j) * a.out_tok + (int64_t)head * a.out_head;
     if (d < a.D)
-      *reinterpret_cast<uint32_t*>(dst + d) = i ? pack16(v.y * by, v.w * by, a.f16) : pack16(v.x * by, v.z * by, a.f16);
+      *reinterpret_cast<uint32_t*>(dst + d) = i ? pack16(v.y, v.w, a.f16) : pack16(v.x, v.z, a.f16);
     if (a.lse && n == 0 && g == 0)
-      a.lse[(int64_t)(q0 + j) * a.hq + head] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+      a.lse[(int64_t)(q0 + j) * a.hq + head] = total[i] == 0.f ? -INFINITY : (top + log2f(total[i])) * 0.6931471805599453f;
   }
 }
 

@@ -14,7 +14,8 @@ struct Decode8Args {
   float* lse;
   uint32_t* status;
   // partials: two for each CTA (of the unit that it goes on with, and of the one
-  // that goes on in the next); outputs [part][D padded / 16][32 lanes], references (of z) and sums
+  // that goes on in the next); outputs, divided by their sums, [part][D padded / 16][32 lanes],
+  // references (of z) and sums
   float4* part_o;
   float2* part_ml;
   int4* split;  // two for each CTA: {CTAs of the unit that begins in it and goes on (0: none),
