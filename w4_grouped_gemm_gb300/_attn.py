@@ -4,9 +4,10 @@ append to and attention over an 8-bit cache.
 
 Argument marshalling only, as in ``_lib``; the checks here are those the library cannot
 make from addresses: that tensors live on the GPU, their element types, that arrays given by a
-pointer alone (indices, lengths, scales, lse) hold as many elements as the call's dims say, and
-that the heads of the tensors that dims were made from are the cache's.  An int in a tensor's
-place is taken as an address, unchecked.
+pointer alone (indices, lengths, scales, lse) hold as many elements as the call's dims say, that
+the heads of the tensors that dims were made from are the cache's, and, of the 8-bit cache's
+operators, that q, k, v and the outputs reach as far as the dims do.  An int in a tensor's place
+is taken as an address, unchecked.
 """
 from __future__ import annotations
 
@@ -132,11 +133,27 @@ def _array_at(what, t, dtype, n):
     _not_taken(what, t, dtype, n)
 
 
-def _not_taken(what, t, dtype, n):
+def _reach_at(what, t, dtype, n):
+    """Address of a GPU tensor of this type whose memory goes on for n elements or more from its
+    first one, whatever its strides; an address as it is; None stays."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.is_cuda and t.dtype is dtype and ((t.numel() >= n and t.is_contiguous()) or _reach(t) >= n):
+        return t.data_ptr()
+    _not_taken(what, t, dtype, n, strided=True)
+
+
+def _reach(t):
+    return t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+
+
+def _not_taken(what, t, dtype, n, strided=False):
     if not t.is_cuda:
         _refuse(f"{what}: a tensor is not on the GPU")
     if t.dtype is not dtype:
         _refuse(f"{what}: a tensor of {t.dtype} where {dtype} belongs")
+    if strided:
+        _refuse(f"{what}: a tensor ends before the {n} elements that the dims reach over")
     _refuse(f"{what}: an array must be contiguous, of {n} elements or more")
 
 
@@ -346,10 +363,15 @@ def lily_attn_rope_append8(dims: RopeDims, cache: PagedCache8, q, k, v, position
     dt, T = _step_type(what, q, k, v, q_out), dims.T
     if dims.D is not None and (dims.D != cache.D or dims.hkv not in (None, cache.heads)):
         _refuse(f"{what}: the dims' heads are not the cache's")
+    last, hq, hkv, D = T - 1, dims.n_q_heads - 1, cache.heads - 1, cache.D
     rc = _L().lily_attn_rope_append8(
-        dims._at, cache.c._at, _DTYPES[dt], _at(what, q, dt), _at(what, k, dt), _at(what, v, dt),
+        dims._at, cache.c._at, _DTYPES[dt],
+        _reach_at(what, q, dt, last * dims.q_token_stride + hq * dims.q_head_stride + D),
+        _reach_at(what, k, dt, last * dims.k_token_stride + hkv * dims.k_head_stride + D),
+        _reach_at(what, v, dt, last * dims.v_token_stride + hkv * dims.v_head_stride + D),
         _array_at(what, positions, torch.int32, T), _array_at(what, slots, torch.int64, T),
-        _array_at(what, inv_freq, torch.float64, dims.rotary_dim // 2), _at(what, q_out, dt),
+        _array_at(what, inv_freq, torch.float64, dims.rotary_dim // 2),
+        _reach_at(what, q_out, dt, last * dims.qo_token_stride + hq * dims.qo_head_stride + D),
         _at(what, ws, ws.dtype), ws.numel() * ws.element_size(), _on(stream, ws))
     if rc:
         _check(rc, what)
@@ -367,10 +389,14 @@ def lily_attn_decode8(dims: AttnDims, cache: PagedCache8, q, q_start, seq_lens, 
     dt, i32, n = _step_type(what, q, out), torch.int32, dims.n_seqs
     if dims.D is not None and dims.D != cache.D:
         _refuse(f"{what}: the dims' heads are not the cache's")
+    last, heads, D = dims.n_tokens - 1, dims.n_q_heads - 1, cache.D
     rc = _L().lily_attn_decode8(
-        dims._at, cache.c._at, _DTYPES[dt], _at(what, q, dt), _array_at(what, q_start, i32, n + 1),
-        _array_at(what, seq_lens, i32, n), _array_at(what, block_table, i32, n * dims.table_stride),
-        _at(what, out, dt), _array_at(what, lse, torch.float32, dims.n_tokens * dims.n_q_heads),
+        dims._at, cache.c._at, _DTYPES[dt],
+        _reach_at(what, q, dt, last * dims.q_token_stride + heads * dims.q_head_stride + D),
+        _array_at(what, q_start, i32, n + 1), _array_at(what, seq_lens, i32, n),
+        _array_at(what, block_table, i32, n * dims.table_stride),
+        _reach_at(what, out, dt, last * dims.out_token_stride + heads * dims.out_head_stride + D),
+        _array_at(what, lse, torch.float32, dims.n_tokens * dims.n_q_heads),
         _at(what, ws, ws.dtype), ws.numel() * ws.element_size(), _on(stream, q))
     if rc:
         _check(rc, what)

@@ -2,8 +2,8 @@
 include/lily_decode.h): projections of a few rows by 4-bit weights, and token sampling.
 
 Argument marshalling only, as in ``_lib``; the checks here are those the library cannot make
-from addresses: that tensors live on the GPU, their element types, and that they hold what the
-call's dims say.  An int in a tensor's place is taken as an address, unchecked.
+from addresses: that tensors live on the GPU, their element types, and that their memory reaches
+as far as the call's dims do.  An int in a tensor's place is taken as an address, unchecked.
 """
 from __future__ import annotations
 
@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._attn import _array_at, _at, _code, _on, _refuse, _Struct
+from ._attn import _array_at, _at, _code, _on, _reach_at, _refuse, _Struct
 from ._lib import _check
 
 # Every symbol include/lily_decode.h declares.
@@ -94,8 +94,10 @@ def lily_decode_linear(dims: LinearDims, x, w: W4Matrix, y, stream=None):
     if (dims.K, dims.N, dims.group) != (w.K, w.N, w.group):
         _refuse(f"{what}: the dims are another matrix's")
     xt, yt = dims.types or (x.dtype, y.dtype)
-    rc = _L().lily_decode_linear(dims._at, _at(what, x, xt), w._q, w._s, w._b, _at(what, y, yt),
-                                 _on(stream, x))
+    last = dims.T - 1
+    rc = _L().lily_decode_linear(
+        dims._at, _reach_at(what, x, xt, last * dims.x_stride + dims.K), w._q, w._s, w._b,
+        _reach_at(what, y, yt, last * dims.out_stride + dims.N), _on(stream, x))
     if rc:
         _check(rc, what)
 
@@ -114,7 +116,8 @@ def lily_decode_sample(dims: SampleDims, logits, temperature, top_k, top_p, min_
     what = "lily_decode_sample"
     f32, i32, n = torch.float32, torch.int32, dims.B
     rc = _L().lily_decode_sample(
-        dims._at, _at(what, logits, dims.type or logits.dtype), _array_at(what, temperature, f32, n),
+        dims._at, _reach_at(what, logits, dims.type or logits.dtype, (n - 1) * dims.stride + dims.V),
+        _array_at(what, temperature, f32, n),
         _array_at(what, top_k, i32, n), _array_at(what, top_p, f32, n),
         _array_at(what, min_p, f32, n), _array_at(what, u, f32, n),
         _array_at(what, tokens, i32, n), _array_at(what, logprobs, f32, n),
