@@ -136,9 +136,13 @@ class TokenModel:
         pages = torch.gather(self.table.long(), 1, (at // self.page).clamp(max=self.table.shape[1] - 1)[:, None])[:, 0]
         return torch.where(at < self.room, pages * self.page + at % self.page, -1)
 
+    def embed(self):
+        """The tokens' rows; row 0 for a sequence that got none (-1: its logits were nothing but -infinity or NaN)."""
+        torch.index_select(self.embedding, 0, self.tokens.clamp(min=0), out=self.residual)
+
     def step(self):
         """self.tokens to the next ones, in place."""
-        torch.index_select(self.embedding, 0, self.tokens, out=self.residual)
+        self.embed()
         slots, positions = self.slots(), self.seq_lens.clone()
         self.seq_lens += 1
         y = None

@@ -142,3 +142,18 @@ def test_a_sequence_whose_room_is_full(oracle_lib):
         assert m.status() == (lily.LILY_STATUS_BAD_LEN if 16 in lens else 0)
         said.append((m.tokens[[0, 2]].tolist(), m.logits[[0, 2]].clone()))
     assert said[0][0] == said[1][0] and torch.equal(said[0][1], said[1][1])
+
+
+def test_a_sequence_without_a_token(oracle_lib):
+    """-1, which the sampler gives for a row of nothing, steps as token 0 does; the others are what they are."""
+    from token_step import TokenModel
+    said = []
+    for token in (-1, 0):
+        m = TokenModel(seqs=3, room=16, seed=9)
+        m.tokens.copy_(torch.tensor([10, token, 30]))
+        m.u.fill_(0.4)
+        m.step()
+        torch.cuda.synchronize()
+        assert m.status() == 0
+        said.append((m.tokens.tolist(), m.logits.clone()))
+    assert said[0][0] == said[1][0] and torch.equal(said[0][1], said[1][1])
