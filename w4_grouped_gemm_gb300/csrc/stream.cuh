@@ -1,5 +1,6 @@
-// stream.cuh -- what kernels share in which each warp streams its data through a
-// ring of its own (cp.async: no barrier, no other warp) into mma.sync.
+// stream.cuh -- what the kernels share that bring packed codes through a ring in
+// shared memory into mma.sync (decode_linear.cuh, attn_decode8.cu): cp.async copies,
+// loads from shared memory, products of 16-bit operands.
 #pragma once
 #include "common.cuh"
 
@@ -41,11 +42,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return __uint_as_float((uint32_t)v << 16);
 }
 
 template <bool F16>
