@@ -866,14 +866,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 }  // namespace
 
 // CTAs of a row's cluster: enough that two CTAs fit on an SM (20480 logits each), and
-// more while there are SMs without a row and a CTA keeps 2048 logits.  16 only for a few
-// rows, or where a row takes them, since few clusters of that size find room at once (top-p
-// of 131072 logits: one row 19.5 us by 16, 23.9 by 8, 33.9 by 4; 16 rows 45, 35, 40).
+// twice as many while every CTA then has an SM of its own, since two on one take turns, and
+// 2048 logits or more.  By top-p, in a graph: 14 rows of 20000 logits 15.3 us by 8 CTAs, 15.4
+// by 4; 18 rows 17.3, 15.5; 36 rows 27.2, 17.3, and 19.2 by 2; 40 rows 20.9 by 4, 19.2 by 2;
+// 76 rows 19.7 by 2, 26.5 by 1; 80 rows 25.9, 26.5.  (1250 logits a CTA: 8 rows of 10000 12.4
+// us by 8, 13.4 by 4; 18 rows 14.8, 13.6.)  16 only for a few rows, or where a row takes them,
+// since few clusters of that size find room at once: 4 rows of 131072 22.5 us by 16, 27.5 by
+// 8; 8 rows 30.2, 27.7.  (Six find room on the GPU that this was measured on, and other GPUs
+// of its kind may place fewer.)
 static int cluster_of(int B, int V, int sms) {
   int C = 1;
   while (C < kMaxCluster && V > C * 20480) C *= 2;
   const int most = B <= 4 ? kMaxCluster : kMaxCluster / 2;
-  while (C < most && (int64_t)B * C * 2 <= 2 * sms && V >= C * 2 * 2048) C *= 2;
+  while (C < most && (int64_t)B * C * 2 <= sms && V >= C * 2 * 2048) C *= 2;
   return C;
 }
 
