@@ -110,6 +110,16 @@ __device__ __forceinline__ float unit8(float x, float scale, float inverse) {
   const float q = x * inverse;
   return inverse > 0.f ? fmaf(fmaf(-q, scale, x), inverse, q) : 0.f;
 }
+// Heads of small numbers: the residue above would fall below fp32's least number (codes
+// differ where the scale is below 2^-114), so they and their scale are taken 2^64 times as large.
+__device__ __forceinline__ bool small8(float scale) { return scale < 0x1p-90f; }
+template <int N>
+__device__ __forceinline__ void lift8(float (&a)[N], float (&b)[N], float& scale, float& inverse) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) a[e] *= 0x1p64f, b[e] *= 0x1p64f;
+  scale *= 0x1p64f;
+  inverse *= 0x1p-64f;
+}
 __device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 __device__ __forceinline__ int64_t scale_cell(const RopeArgs& a, int64_t slot) {
   return (slot >> a.page_shift) * a.s_page + (slot & ((1 << a.page_shift) - 1)) * a.s_tok;
@@ -303,7 +313,9 @@ __global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 1)
       const uint32_t mask = (lanes == 32 ? ~0u : (1u << lanes) - 1) << (threadIdx.x & 31 & ~(lanes - 1));
       for (uint32_t o = lanes >> 1; o > 0; o >>= 1) size = max(size, __shfl_xor_sync(mask, size, o));
       float inverse;
-      const float scale = scale8(size, inverse);
+      float scale = scale8(size, inverse);
+      if (u == 0) (v ? a.vs : a.ks)[scale_cell(a, tb.slot[i]) + (v ? h - a.hkv : h) * a.s_head] = scale;
+      if (small8(scale)) lift8(fa, fb, scale, inverse);
       uint8_t* to = static_cast<uint8_t*>(v ? a.vc : a.kc) + (v ? h - a.hkv : h) * a.c_head + tb.cell[i];
       auto put = [&](const float(&x)[8], int at) {
         uint32_t w[2];
@@ -315,7 +327,6 @@ __global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 1)
       };
       if (oa >= 0) put(fa, oa);
       if (ob >= 0) put(fb, ob);
-      if (u == 0) (v ? a.vs : a.ks)[scale_cell(a, tb.slot[i]) + (v ? h - a.hkv : h) * a.s_head] = scale;
     }
   }
 }
@@ -376,8 +387,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a,
         }
         size = __reduce_max_sync(0xffffffffu, size);
         float inverse;
-        const float scale = scale8(size, inverse);
+        float scale = scale8(size, inverse);
         const int64_t kv = h - (is_v ? hk : a.hq);
+        if (lane == 0) (is_v ? a.vs : a.ks)[scale_cell(a, slot) + kv * a.s_head] = scale;
+        if (small8(scale)) lift8(p, r, scale, inverse);
         uint8_t* to = static_cast<uint8_t*>(is_v ? a.vc : a.kc) + cell + kv * a.c_head;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -391,7 +404,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a,
             to[u - pairs + (is_v ? 0 : a.rot)] = (uint8_t)both;
           }
         }
-        if (lane == 0) (is_v ? a.vs : a.ks)[scale_cell(a, slot) + kv * a.s_head] = scale;
         continue;
       }
       for (int u = lane; u < units; u += lanes) {
