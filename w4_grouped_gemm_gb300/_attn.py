@@ -349,11 +349,14 @@ def lily_attn_shared_prefix(dims: AttnDims, cache: PagedCache, q, prefix_pages, 
 
 
 def _step_type(what, *tensors):
-    """The 16-bit type that a call's tensors share (None and addresses aside)."""
-    types = {t.dtype for t in tensors if t is not None and t.__class__ is not int}
-    if len(types) != 1 or not types <= {torch.bfloat16, torch.float16}:
-        _refuse(f"{what}: tensors of one 16-bit type belong here, not {sorted(map(str, types))}")
-    return types.pop()
+    """The 16-bit type of the first of a call's tensors (None and addresses aside), which the
+    others are held to."""
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            if t.dtype is torch.bfloat16 or t.dtype is torch.float16:
+                return t.dtype
+            _refuse(f"{what}: tensors of one 16-bit type belong here, not {t.dtype}")
+    _refuse(f"{what}: tensors of one 16-bit type belong here")
 
 
 def lily_attn_rope_append8(dims: RopeDims, cache: PagedCache8, q, k, v, positions, slots, inv_freq,
