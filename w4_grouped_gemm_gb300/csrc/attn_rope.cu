@@ -134,8 +134,10 @@ __device__ __forceinline__ int64_t scale_cell(const RopeArgs& a, int64_t slot) {
 // and before the slots and sines are looked up.  (Addresses worked out anew for
 // each 16 bytes bound the kernel by its instructions: 217 per 512 bytes, 56 us
 // for 8192 tokens of 20 heads of 256.)
+// (The 16-bit kernels name no least number of blocks on an SM: with one block the compiler
+// took 108 to 145 registers in place of 64 to 104, and 8192 such tokens 39.5 us in place of 32.9.)
 template <bool Q8, int STYLE, bool F16, int NI>
-__global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 1)
+__global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 0)
     rope_append_runs_kernel(const RopeArgs a, int tok_per_cta, int lanes_log2) {
   constexpr int NB = 4 / NI;
   __shared__ Tables tb;
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 1)
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
       const int h = h0 + first + n * step;
-      kind[n] = h >= H ? 0 : Q8 || h < a.hq ? 1 : h < hk ? 2 : 3;
+      kind[n] = h < a.hq ? 1 : Q8 ? 0 : h < hk ? 2 : h < H ? 3 : 0;
       src[n] = nullptr;
       dst[n] = nullptr;
       src_tok[n] = 0;
@@ -222,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, Q8 ? NI == 4 ? 2 : 4 : 1)
         if (i >= nt) break;
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-          if (kind[n] > 1 && tb.slot[i] < 0) continue;
           uint16_t* to = dst[n] + (kind[n] == 1 ? (int64_t)i * a.qo_tok : tb.cell[i]);
+          if (kind[n] > 1 && tb.slot[i] < 0) continue;
           if (turns && kind[n] != 3) {
             uint32_t wa[4] = {xa[j][n].x, xa[j][n].y, xa[j][n].z, xa[j][n].w};
             uint32_t wb[4] = {xb[j][n].x, xb[j][n].y, xb[j][n].z, xb[j][n].w};
