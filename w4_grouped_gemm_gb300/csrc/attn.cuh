@@ -145,28 +145,36 @@ struct SeqInfo {
   int q0, qn, len;
   bool bad;
 };
-// From its first query token, the one after its last, and its length as they were given.
-__device__ __forceinline__ SeqInfo seq_held(const AttnSet& s, int T, int q0, int q1, int len) {
-  SeqInfo r;
-  r.bad = false;
-  r.q0 = q0;
+// r.q0, and q1, the token after its last, and r.len, as they were given.
+__device__ __forceinline__ void hold_tokens(SeqInfo& r, const AttnSet& s, int T, int q1) {
   if (r.q0 < 0 || r.q0 > T || q1 < r.q0 || q1 > T || q1 - r.q0 > s.max_q_len) {
     r.bad = true;
     r.q0 = min(max(r.q0, 0), T);
     q1 = min(max(q1, r.q0), min(T, r.q0 + s.max_q_len));
   }
   r.qn = q1 - r.q0;
-  r.len = len;
+}
+__device__ __forceinline__ void hold_len(SeqInfo& r, const AttnSet& s) {
   if (r.len < 0 || r.len > s.max_len) {
     r.bad = true;
     r.len = min(max(r.len, 0), s.max_len);
   }
-  return r;
 }
 __device__ __forceinline__ SeqInfo seq_info(const AttnSet& s, int T, int i) {
-  const int q0 = s.q_start ? s.q_start[i] : i * s.max_q_len;
-  const int q1 = s.q_start ? s.q_start[i + 1] : q0 + s.max_q_len;
-  return seq_held(s, T, q0, q1, s.lens ? s.lens[i] : s.max_len);
+  SeqInfo r;
+  r.bad = false;
+  int q1;
+  if (s.q_start) {
+    r.q0 = s.q_start[i];
+    q1 = s.q_start[i + 1];
+  } else {
+    r.q0 = i * s.max_q_len;
+    q1 = r.q0 + s.max_q_len;
+  }
+  hold_tokens(r, s, T, q1);
+  r.len = s.lens ? s.lens[i] : s.max_len;
+  hold_len(r, s);
+  return r;
 }
 
 // ---------------------------------------------------------------- copies, waits, 2^x

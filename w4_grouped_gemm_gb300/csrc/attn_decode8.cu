@@ -116,7 +116,9 @@ struct Cursor {
                      : make_int3(i * s.max_q_len, (i + 1) * s.max_q_len, s.lens[i]);
   }
   __device__ __forceinline__ void load(const AttnSet& s, const Decode8Args& a, int tile_keys, int3 is) {
-    const SeqInfo i = seq_held(s, a.T, is.x, is.y, is.z);
+    SeqInfo i = {is.x, 0, is.z, false};
+    hold_tokens(i, s, a.T, is.y);
+    hold_len(i, s);
     q0 = i.q0;
     qn = i.qn;
     len = i.len;
