@@ -207,7 +207,8 @@ int lily_attn_shared_prefix(const lily_attn_dims* dims, const lily_attn_cache* c
  *   head_dim    a multiple of 16, 16 to 256
  *   strides     of codes: multiples of 16; of scales: 1 or more; below 2^39
  * k and v 16-byte aligned, scales by their elements.  A page's codes are finite
- * (as the append writes them); scales may be any number.
+ * (as the append writes them); scales may be any finite number, or NaN, which spoils
+ * the rows that see its key.
  */
 typedef struct {
   void* k;
@@ -242,12 +243,13 @@ size_t lily_attn_decode8_workspace_bytes(const lily_attn_dims* dims, const lily_
  *   dims    prefix_len is 0; sequences that share pages name them in their tables
  *   dtype   BF16 or F16: type of q and out
  *   q_start, seq_lens, block_table, lse  as lily_attn_shared_prefix's
- * Scores, softmax statistics and sums are fp32; a probability times its key's value
- * scale is rounded to fp16, held so that one 2^-24 times the largest value scale
- * still keeps all its bits.  A row that sees nothing is 0 with lse -infinity; tokens
- * of no sequence are left as they were.  Bad page indices, lengths and ranges are
- * treated as by lily_attn_shared_prefix, and outputs are otherwise the same bits on
- * every run with the same arguments. */
+ * Scores, softmax statistics and sums are fp32, and scores stay below 2^27 in size, as
+ * there; a probability times its key's value scale is rounded to fp16, held so that one
+ * 2^-24 times the largest value scale, whatever that is, still keeps all its bits.  A
+ * row that sees nothing is 0 with lse -infinity; tokens of no sequence are left as they
+ * were.  Bad page indices, lengths and ranges are treated as by
+ * lily_attn_shared_prefix, and outputs are otherwise the same bits on every run with
+ * the same arguments. */
 int lily_attn_decode8(const lily_attn_dims* dims, const lily_attn_cache8* cache, int32_t dtype,
                       const void* q, const int32_t* q_start, const int32_t* seq_lens,
                       const int32_t* block_table, void* out, float* lse, void* workspace,

@@ -44,7 +44,7 @@ typedef struct {
  *          in bits 4-7
  *   scale  bf16 [N][K/group]
  *   bias   bf16 [N][K/group]; NULL: -8 times the scale (symmetric weights)
- *   y      [T][N]; 16-byte aligned in its first row
+ *   y      [T][N]; 16-byte aligned in its first row; shares no element with x
  * Products with the codes are exact and summed in fp32, as is everything else;
  * the sum is rounded once.  x of 2^112 or more in size overflows fp32 on the way.
  * A row of x with an infinity or a NaN gives no finite value in that row of y.
@@ -81,7 +81,8 @@ typedef struct {
  *   u            fp32 [B], 0 <= u < 1 (held to that; NaN: 0); NULL: the first of the
  *                order in every row
  *   tokens       int32 [B]
- *   logprobs     fp32 [B] or NULL: the log of the token's share of the kept mass
+ *   logprobs     fp32 [B] or NULL: the log of the token's share of the kept mass; 0 in
+ *                rows without a draw (temperature 0 or less, or u NULL)
  *   workspace    256 bytes or more (the status word, as lily_attn.h's)
  * The arrays are aligned by their elements; logits by 16 bytes in their first row
  * (rows that do not lie on 16 bytes are read element by element at their ends).

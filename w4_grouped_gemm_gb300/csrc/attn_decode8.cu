@@ -36,11 +36,11 @@
 // leave fp32's range, and partial outputs are divided by their sums.  q is brought to
 // fp16's range by a power of two for each row.
 //
-// Measured: 4 sequences of up to 131072 keys, 2 KV heads of 256, 86 us, 5.8 TB/s; 128 of
-// up to 4096, 97 us, 6.0 TB/s; one of 301 keys 8.2 us, half of it the look-ups before
+// Measured: 4 sequences of up to 131072 keys, 2 KV heads of 256, 84 us, 5.9 TB/s; 128 of
+// up to 4096, 98 us, 5.9 TB/s; one of 301 keys 8.3 us, half of it the look-ups before
 // the first tile (lengths, pages, keys one after another) and the joining.  A tile is some
 // 1800 cycles of a CTA, a unit's end and next beginning some 4000, which bounds short
-// sequences (256 of up to 300 keys: 39 us).
+// sequences (256 of up to 300 keys: 40 us).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -428,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
     int ev = -127;                 // exponent of the largest v_scale so far
-    float2 fv = power2(10 - ev);   // 2^(10 - ev)
-    float next_v = 1.17549435e-38f;  // 2^(ev + 1): a scale of that size moves ev
+    float2 fv = power2(10 - ev);
+    float next_v = 0x1p-126f;      // 2^(ev + 1): a scale of that size moves ev
 
     const int n_tiles = min(left, out.tiles - out.tile);
 #pragma unroll 1

@@ -22,9 +22,10 @@
 //
 // Instructions and barriers bound it, not HBM.  Measured: 128 rows of 131072 by top-p
 // 142 us (0.47 TB/s; 180 instructions a logit, 61 percent of issue slots, four rounds of
-// 38 clusters), by all filters 67, by none 55; one row with all filters 13.7; 17 rows of
-// 50021 in bf16 19.7.  A first pass that only counts logits by step and a second that
-// adds masses up exactly and lists the steps about p took 132 us, and no less for few rows.
+// 38 clusters), by all filters 66, by none 55; one row with all filters 13.6; 17 rows of
+// 50021 in bf16 20 to 24, by the inputs.  A first pass that only counts logits by step and
+// a second that adds masses up exactly and lists the steps about p took 132 us, and no less
+// for few rows.
 #include <algorithm>
 #include <cfloat>
 
