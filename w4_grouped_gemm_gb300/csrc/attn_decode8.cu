@@ -33,8 +33,11 @@
 // is held 2^(10 - e) times as large, e the exponent of the largest v_scale so far, so
 // that it ends below 2^15 and all bits are kept from 2^-24 of the reference on.  e may be
 // that of any fp32 number: powers of two by it are taken in two factors where one would
-// leave fp32's range, and partial outputs are divided by their sums.  q is brought to
-// fp16's range by a power of two for each row.
+// leave fp32's range, and partial outputs are divided by their sums.  The rounding is what
+// an operand of 16 bits costs (a second product with what it took off would be half of all
+// MMAs more): with fp16 outputs the error against 64 bits is 2.9e-4, where fp32 throughout
+// gives 2.1e-4, and bf16 outputs round away more.  q is brought to fp16's range by a power of
+// two for each row.
 //
 // Measured: 4 sequences of up to 131072 keys, 2 KV heads of 256, 84 us, 5.9 TB/s; 128 of
 // up to 4096, 98 us, 5.9 TB/s; one of 301 keys 8.3 us, half of it the look-ups before
